@@ -63,7 +63,8 @@ typedef enum {
   VSWIN_ERR_CUDA = 3,         /* a CUDA runtime call or launch failed */
   VSWIN_ERR_TIMEOUT = 4,      /* a kernel's bounded wait gave up (reported by vswin_poll_error) */
   VSWIN_ERR_NO_MEMORY = 5,    /* scratch allocation failed */
-  VSWIN_ERR_BOUNDS = 6        /* a build with VSWIN_DEBUG_BOUNDS caught an index out of its extent */
+  VSWIN_ERR_BOUNDS = 6        /* an index out of its extent: caught by a build with VSWIN_DEBUG_BOUNDS, or read from
+                                 the device by an operator over sequences (reported by vswin_poll_error) */
 } vswin_status;
 
 /*
@@ -295,6 +296,171 @@ int vswin_wmsa_forward_noalloc(const void* x, int B, int T, int H, int W, int C,
                                const void* bias_table, void* out, void* stream);
 
 /*
+ * Operators over token sequences: the norm of queries and keys for each head
+ * with the position rotation, and attention with a learned relative-position
+ * bias by buckets. Where the layer's table (step 5 above) holds one value for
+ * each offset inside a window, the buckets bound it for sequences of any
+ * length: near offsets have a bucket each, far ones share them.
+ *
+ * Element types; F32 where an entry says so.
+ */
+typedef enum { VSWIN_BF16 = 0, VSWIN_FP16 = 1, VSWIN_F32 = 2 } vswin_dtype;
+
+/* A (batch, token, head, channel) tensor on the device: channels contiguous,
+ * the other strides in elements (any order; q, k and v may be slices of one
+ * projection's output). An output may not hold one element twice; an input may
+ * (stride 0). Strides of dimensions of extent 1 are not looked at. */
+typedef struct {
+  void* data;
+  long long batch_stride, token_stride, head_stride;
+} vswin_heads;
+
+/* Rotation of the first `dim` channels (even): pairs (i, i + dim/2), or (2i,
+ * 2i+1) when `interleaved`, turn by the angle whose cosine and sine stand in
+ * row `position` of two float tables [rows][dim/2]. positions: int [B][L]
+ * contiguous on the device, or NULL (token l has position l, rows >= L). A
+ * position outside [0, rows) turns by the nearest row and is reported by
+ * vswin_poll_error (VSWIN_ERR_BOUNDS). */
+typedef struct {
+  const float* cos;
+  const float* sin;
+  int rows, dim, interleaved;
+  const int* positions;
+} vswin_rotation;
+
+/*
+ * Norm and rotation of queries (hq heads) and keys (hk heads) in one pass:
+ *   n = x / sqrt(mean_c(x^2) + eps) * gamma over the d channels of a head,
+ *   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin) on the rotated pairs.
+ * gamma_q, gamma_k [d] of the tensors' type (any dtype). d up to 256; rotation
+ * may be NULL. q_out may be q itself and k_out k itself (the same view), else
+ * they overlap neither. Arithmetic in fp32, one rounding. 16-byte loads when d
+ * and dim are multiples of 16 and every row starts on 16 bytes, element by
+ * element otherwise. No scratch.
+ */
+int vswin_qk_norm_forward(int dtype, int B, int L, int hq, int hk, int d, const vswin_heads* q, const vswin_heads* k,
+                          const void* gamma_q, const void* gamma_k, float eps, const vswin_rotation* rotation,
+                          const vswin_heads* q_out, const vswin_heads* k_out, void* stream);
+
+/*
+ * Its gradient for output gradients dq_out, dk_out: dq, dk (type of q; may be
+ * the same view as the input or the output gradient they come from) and
+ * dgamma_q, dgamma_k (float [d], overwritten). Deterministic: the rows' shares
+ * of dgamma are added in a fixed order. Scratch: 4 d bytes per block of the
+ * launch (at most a few hundred KB), from the library's pool.
+ */
+int vswin_qk_norm_backward(int dtype, int B, int L, int hq, int hk, int d, const vswin_heads* q, const vswin_heads* k,
+                           const void* gamma_q, const void* gamma_k, float eps, const vswin_rotation* rotation,
+                           const vswin_heads* dq_out, const vswin_heads* dk_out, const vswin_heads* dq,
+                           const vswin_heads* dk, float* dgamma_q, float* dgamma_k, void* stream);
+
+/*
+ * Host helper: bucket of each offset (key - query) in [-max_distance,
+ * max_distance], 2 max_distance + 1 ints. Of a side's buckets (all of them, or
+ * half of them for each sign when bidirectional) the first half are single
+ * distances 0, 1, ...; the others split the distances up to max_distance evenly
+ * in the logarithm, and the last also holds all beyond. Offsets > 0 take the
+ * upper half of the buckets (bidirectional) or bucket 0.
+ */
+int vswin_bucket_map(int buckets, int max_distance, int bidirectional, int* map);
+
+/* The bias: table [buckets][hq] of the tensors' type, map int
+ * [2 max_distance + 1] on the device (vswin_bucket_map's or any other), offsets
+ * beyond max_distance read its ends. buckets up to 4096, max_distance up to
+ * 2^20. A bias at or below -1e30 takes the key out of the softmax. A map entry
+ * outside [0, buckets) counts as bias 0 and is reported by vswin_poll_error
+ * (VSWIN_ERR_BOUNDS). */
+typedef struct {
+  const void* table;
+  const int* map;
+  int buckets, max_distance;
+} vswin_bucket_bias;
+
+/* Which keys a query sees. All arrays int [B] on the device, or NULL:
+ * q_lens (Lq), kv_lens (Lk) how many rows and keys of a sequence take part,
+ * q_start (0) the position of its query 0; query i stands at q_start + i, key j
+ * at j. causal: key j is seen up to j <= q_start + i. What lies behind the
+ * lengths is never used, whatever it holds. Lengths outside [0, Lq] or [0, Lk]
+ * are clamped and reported by vswin_poll_error (VSWIN_ERR_BOUNDS). */
+typedef struct {
+  const int* q_lens;
+  const int* kv_lens;
+  const int* q_start;
+  int causal;
+} vswin_visibility;
+
+/*
+ * Attention with the bucketed bias, for query head h with key head h hk / hq:
+ *   s_ij = scale q_i . k_j + table[map[clip(j - q_start - i)]][h]
+ *   out_i = sum_j softmax_j(s_ij) v_j,  lse_i = log sum_j exp(s_ij)
+ * over the keys that query i sees. Rows at or behind q_lens, and rows that see
+ * no key, have out 0 and lse -inf.
+ * q, out (B, Lq, hq, d); k, v (B, Lk, hk, d); bf16 or fp16; d 32, 64 or 128;
+ * hq a multiple of hk; pointers and strides multiples of 16 bytes. lse float
+ * [B][hq][Lq]. vis may be NULL (everything is seen). out overlaps no input.
+ * Products accumulate in fp32 on the tensor cores, softmax statistics in fp32;
+ * the probabilities are rounded to the tensors' type as operands. The result is
+ * the same for the same call. Scratch: none, or partial results of a split of
+ * the keys when there are few rows, from the library's pool.
+ */
+int vswin_bias_attention_forward(int dtype, int B, int Lq, int Lk, int hq, int hk, int d, const vswin_heads* q,
+                                 const vswin_heads* k, const vswin_heads* v, float scale, const vswin_bucket_bias* bias,
+                                 const vswin_visibility* vis, const vswin_heads* out, float* lse, void* stream);
+
+/*
+ * Its gradient for output gradient dout, from the forward's out and lse: dq
+ * (B, Lq, hq, d), dk, dv (B, Lk, hk, d; summed over the heads that share them)
+ * and dtable [buckets][hq], all of the tensors' type, summed in fp32 and rounded
+ * once, overwritten. Zero for rows and keys that take no part. The gradients
+ * overlap no input; dq, dk and dv may be slices of one buffer. Scratch: from the
+ * library's pool, 4 bytes per query row and head plus the table's sums.
+ */
+int vswin_bias_attention_backward(int dtype, int B, int Lq, int Lk, int hq, int hk, int d, const vswin_heads* q,
+                                  const vswin_heads* k, const vswin_heads* v, float scale,
+                                  const vswin_bucket_bias* bias, const vswin_visibility* vis, const vswin_heads* out,
+                                  const float* lse, const vswin_heads* dout, const vswin_heads* dq,
+                                  const vswin_heads* dk, const vswin_heads* dv, void* dtable, void* stream);
+
+/*
+ * AdamW over many tensors, what the backward entries' gradients are for:
+ *   g' = g * grad_scale,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32. A tensor's n elements are contiguous in each of its buffers. param
+ * (any dtype) is rounded from the result; with master (float, may be NULL) the
+ * step is done on master and param is its rounded copy. grad: any dtype.
+ * bits 32: m and v are float [n], the scales are not looked at. bits 8: m is
+ * signed char [n], v unsigned char [n], each block of 256 elements with one
+ * scale (float [ceil(n / 256)], the block's largest value):
+ *   m = m_scale sgn(c) (c / 127)^2,  v = v_scale (c / 255)^4,
+ * rounded to the nearest code in that spacing; a positive v never reads back as
+ * zero. All-zero codes and scales are zero moments.
+ * The list is a host array and is not kept; its records travel with the launch
+ * (one launch per 192 tensors), so that a step can be captured. A captured step
+ * takes its count from step_device (one int on the device, from 1; `step` is
+ * then not looked at) and, as any step may, the factor of the gradients from
+ * grad_scale (one float on the device, or NULL). A tensor's buffers may not
+ * overlap one another; two tensors of a list may not share buffers (not checked).
+ */
+typedef struct {
+  void* param;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  long long n;
+  double weight_decay;
+  int param_dtype, grad_dtype;
+} vswin_adamw_tensor;
+int vswin_adamw_step(const vswin_adamw_tensor* tensors, int count, int bits, double lr, double beta1, double beta2,
+                     double eps, long long step, const int* step_device, const float* grad_scale, void* stream);
+
+/* The values that 8-bit moments of n elements stand for, as out_dtype. */
+int vswin_adamw_decode(const void* m, const float* m_scale, const void* v, const float* v_scale, long long n,
+                       int out_dtype, void* m_out, void* v_out, void* stream);
+
+/*
  * Index maps of the layer, written to caller-allocated device int32 buffers
  * (any of them may be NULL to skip it). They spell out steps 1-3 and 5 above:
  * the padding and cyclic shift of the token grid and the window partition
@@ -326,7 +492,8 @@ const char* vswin_last_error(void);
  * Synchronises `stream`, then returns and clears the device error word:
  * VSWIN_OK, or VSWIN_ERR_TIMEOUT if a kernel's bounded wait gave up since the
  * last poll, VSWIN_ERR_BOUNDS if a build with VSWIN_DEBUG_BOUNDS caught an
- * index out of its extent (the access was skipped), or VSWIN_ERR_CUDA if
+ * index out of its extent (the access was skipped) or, in every build, a
+ * position, length or bucket read from the device was out of range, or VSWIN_ERR_CUDA if
  * synchronisation failed.
  */
 int vswin_poll_error(void* stream);

@@ -6,9 +6,15 @@ The layer runs in ``libvswin.so`` (hand-written CUDA for sm_100a, C ABI in
 
 from . import vswin  # noqa: F401
 from .vswin import (  # noqa: F401
+    AdamW,
     VswinError,
+    bias_attention_backward,
+    bias_attention_forward,
+    bucket_map,
     clamp_window,
     index_maps,
+    qk_norm_backward,
+    qk_norm_forward,
     wmsa_forward,
     wmsa_forward_f32,
     wmsa_forward_host,

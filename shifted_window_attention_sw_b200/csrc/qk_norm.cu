@@ -1,0 +1,501 @@
+// Norms of queries and keys for each head with the position rotation in the
+// same pass, and its gradient. For a head's channels x[0..d):
+//
+//   r = 1 / sqrt(mean(x^2) + eps),  n = x r gamma,
+//   y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin
+//
+// for the channel pairs (a, b) of the first `rot` channels ((i, i + rot/2), or
+// (2i, 2i+1) when interleaved), y = n for the rest; cos and sin come from the
+// row of a table that the token's position names. The rotation is orthogonal,
+// so with g = R^T dy:
+//
+//   dgamma = sum over rows of g x r,   h = g gamma,
+//   dx = r (h - x r mean(h x r)).
+//
+// Both directions are bound by HBM: forward reads x and writes y once, backward
+// reads x and dy and writes dx. Vector path: a row is held by d/16 lanes, each
+// with 16 channels as eight (a, b) pairs in registers, so that the rotation
+// needs no exchange between lanes; consecutive lanes take consecutive rows, and
+// two rows per lane are in flight. Rows whose width, alignment or rotation does
+// not split into 16-byte pieces (the rule is vec_ok) go one row per warp,
+// element by element.
+#include "sequence.h"
+
+namespace vswin {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxD = 256;
+
+template <class T>
+struct Vec8 {  // 8 elements, 16-byte pieces
+  static constexpr int N = sizeof(T) * 8 / 16;
+  uint4 u[N];
+};
+template <class T>
+__device__ __forceinline__ void load8(const T* p, Vec8<T>& v) {
+#pragma unroll
+  for (int k = 0; k < Vec8<T>::N; ++k) v.u[k] = reinterpret_cast<const uint4*>(p)[k];
+}
+template <class T>
+__device__ __forceinline__ void unpack8(const Vec8<T>& v, float (&f)[8]) {
+  const T* e = reinterpret_cast<const T*>(v.u);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = to_f(e[k]);
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
+  Vec8<T> v;
+  T* e = reinterpret_cast<T*>(v.u);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) e[k] = from_f<T>(f[k]);
+#pragma unroll
+  for (int k = 0; k < Vec8<T>::N; ++k) reinterpret_cast<uint4*>(p)[k] = v.u[k];
+}
+
+// Row of the angle tables for token (b, l); a position outside the tables is
+// recorded in the error word and the nearest row is used.
+__device__ __forceinline__ long long angle_row(const QkNormArgs& a, int b, int l) {
+  if (!a.positions) return l;
+  int pos = a.positions[(long long)b * a.L + l];
+  if (pos < 0 || pos >= a.rows) {
+    atomicCAS(a.err, 0, kErrBounds);
+    pos = pos < 0 ? 0 : a.rows - 1;
+  }
+  return pos;
+}
+
+// Channels of lane t of a row: two runs of 8, and whether its pairs turn.
+struct LaneChannels {
+  int c0, c1;
+  int angle;  // first of its eight angles, or -1
+  bool inter;
+};
+__device__ __forceinline__ LaneChannels lane_channels(const QkNormArgs& a, int t) {
+  LaneChannels c;
+  c.inter = a.interleaved != 0;
+  const int turned = a.rot / 16;
+  c.angle = t < turned ? 8 * t : -1;
+  if (!c.inter && t < turned) {
+    c.c0 = 8 * t;
+    c.c1 = 8 * t + a.rot / 2;
+  } else {
+    c.c0 = 16 * t;
+    c.c1 = 16 * t + 8;
+  }
+  return c;
+}
+
+// The two runs as pairs: (a, b) = (run 0, run 1), or even and odd channels.
+__device__ __forceinline__ void to_pairs(const LaneChannels& c, float (&a)[8], float (&b)[8]) {
+  if (!c.inter) return;
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    x[k] = a[k];
+    x[8 + k] = b[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    a[k] = x[2 * k];
+    b[k] = x[2 * k + 1];
+  }
+}
+__device__ __forceinline__ void from_pairs(const LaneChannels& c, float (&a)[8], float (&b)[8]) {
+  if (!c.inter) return;
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    x[2 * k] = a[k];
+    x[2 * k + 1] = b[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    a[k] = x[k];
+    b[k] = x[8 + k];
+  }
+}
+
+__device__ __forceinline__ void load_angles(const QkNormArgs& a, const LaneChannels& c, long long row, float (&cs)[8],
+                                            float (&sn)[8]) {
+  if (c.angle >= 0) {
+    const float4* cp = reinterpret_cast<const float4*>(a.cosp + row * (a.rot / 2) + c.angle);
+    const float4* sp = reinterpret_cast<const float4*>(a.sinp + row * (a.rot / 2) + c.angle);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 u = __ldg(cp + k), w = __ldg(sp + k);
+      cs[4 * k] = u.x, cs[4 * k + 1] = u.y, cs[4 * k + 2] = u.z, cs[4 * k + 3] = u.w;
+      sn[4 * k] = w.x, sn[4 * k + 1] = w.y, sn[4 * k + 2] = w.z, sn[4 * k + 3] = w.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) cs[k] = 1.f, sn[k] = 0.f;
+  }
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o, G);
+  return v;
+}
+
+// Rows are numbered (b * L + l) * heads + h. The first `qblocks` blocks walk
+// q's rows, the others k's.
+template <class T, int G, bool kBackward>
+__global__ void __launch_bounds__(kThreads) qk_norm_vec_kernel(QkNormArgs a, int qblocks, float* partial) {
+  const int w = blockIdx.x < qblocks ? 0 : 1;
+  const int block = w ? blockIdx.x - qblocks : blockIdx.x;
+  const int blocks = w ? gridDim.x - qblocks : qblocks;
+  const int heads = a.heads[w];
+  const long long rows = (long long)a.B * a.L * heads;
+  const int t = threadIdx.x % G;
+  const bool live = t < a.d / 16;
+  const LaneChannels c = lane_channels(a, t);
+  const float inv_d = 1.f / (float)a.d;
+  Vec8<T> g0, g1;
+  if (live) {
+    load8(static_cast<const T*>(a.gamma[w]) + c.c0, g0);
+    load8(static_cast<const T*>(a.gamma[w]) + c.c1, g1);
+  }
+  float sum_a[8], sum_b[8];
+  if (kBackward) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum_a[k] = sum_b[k] = 0.f;
+  }
+  const long long per = kThreads / G;  // rows of a block's step
+  // every lane of a warp makes the same number of turns (the sums below are warp-wide)
+  for (long long r0 = (long long)block * per; r0 < rows; r0 += (long long)blocks * per) {
+    const long long row = r0 + threadIdx.x / G;
+    const bool on = live && row < rows;
+    int b = 0, l = 0, h = 0;
+    if (row < rows) {
+      const unsigned tok = (unsigned)((unsigned long long)row < (1ull << 32) ? (unsigned)row / (unsigned)heads
+                                                                             : (unsigned long long)row / heads);
+      h = (int)(row - (long long)tok * heads);
+      b = (int)(tok / (unsigned)a.L);
+      l = (int)(tok - (unsigned)b * (unsigned)a.L);
+    }
+    float xa[8], xb[8], ya[8], yb[8], cs[8], sn[8], ga[8], gb[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) xa[k] = xb[k] = ya[k] = yb[k] = 0.f;
+    if (on) {
+      const T* xp = static_cast<const T*>(a.x[w].p) + a.x[w].at(b, l, h);
+      Vec8<T> u0, u1, d0, d1;
+      load8(xp + c.c0, u0);
+      load8(xp + c.c1, u1);
+      if (kBackward) {
+        const T* yp = static_cast<const T*>(a.y[w].p) + a.y[w].at(b, l, h);
+        load8(yp + c.c0, d0);
+        load8(yp + c.c1, d1);
+      }
+      load_angles(a, c, c.angle >= 0 ? angle_row(a, b, l) : 0, cs, sn);
+      unpack8(u0, xa);
+      unpack8(u1, xb);
+      to_pairs(c, xa, xb);
+      if (kBackward) {
+        unpack8(d0, ya);
+        unpack8(d1, yb);
+        to_pairs(c, ya, yb);
+      }
+      unpack8(g0, ga);
+      unpack8(g1, gb);
+      to_pairs(c, ga, gb);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(xa[k], xa[k], fmaf(xb[k], xb[k], ss));
+    const float r = rsqrtf(group_sum<G>(ss) * inv_d + a.eps);
+    if (!kBackward) {
+      if (on) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float na = xa[k] * r * ga[k], nb = xb[k] * r * gb[k];
+          ya[k] = na * cs[k] - nb * sn[k];
+          yb[k] = nb * cs[k] + na * sn[k];
+        }
+        from_pairs(c, ya, yb);
+        T* yp = static_cast<T*>(a.y[w].p) + a.y[w].at(b, l, h);
+        store8(yp + c.c0, ya);
+        store8(yp + c.c1, yb);
+      }
+    } else {
+      float along = 0.f;
+      if (on) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float gya = ya[k] * cs[k] + yb[k] * sn[k];  // R^T dy
+          const float gyb = yb[k] * cs[k] - ya[k] * sn[k];
+          xa[k] *= r;
+          xb[k] *= r;
+          sum_a[k] = fmaf(gya, xa[k], sum_a[k]);
+          sum_b[k] = fmaf(gyb, xb[k], sum_b[k]);
+          ya[k] = gya * ga[k];
+          yb[k] = gyb * gb[k];
+          along = fmaf(ya[k], xa[k], fmaf(yb[k], xb[k], along));
+        }
+      }
+      along = group_sum<G>(along) * inv_d;
+      if (on) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          ya[k] = r * (ya[k] - xa[k] * along);
+          yb[k] = r * (yb[k] - xb[k] * along);
+        }
+        from_pairs(c, ya, yb);
+        T* dp = static_cast<T*>(a.dx[w].p) + a.dx[w].at(b, l, h);
+        store8(dp + c.c0, ya);
+        store8(dp + c.c1, yb);
+      }
+    }
+  }
+  if (kBackward) {
+    // this block's share of dgamma: lanes of the same channels, then warps, in a fixed order
+    __shared__ float s[kThreads / 32][kMaxD];
+    from_pairs(c, sum_a, sum_b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+      for (int o = 16; o >= G; o >>= 1) {
+        sum_a[k] += __shfl_xor_sync(0xffffffffu, sum_a[k], o);
+        sum_b[k] += __shfl_xor_sync(0xffffffffu, sum_b[k], o);
+      }
+      if (live && (threadIdx.x & 31) < G) {
+        s[threadIdx.x >> 5][c.c0 + k] = sum_a[k];
+        s[threadIdx.x >> 5][c.c1 + k] = sum_b[k];
+      }
+    }
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < a.d; ch += kThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kThreads / 32; ++k) v += s[k][ch];
+      partial[(long long)blockIdx.x * a.d + ch] = v;
+    }
+  }
+}
+
+// One row per warp, element by element: any even rot, width up to kMaxD, any
+// alignment and strides.
+template <class T, bool kBackward>
+__global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(QkNormArgs a, int qblocks, float* partial) {
+  const int w = blockIdx.x < qblocks ? 0 : 1;
+  const int block = w ? blockIdx.x - qblocks : blockIdx.x;
+  const int blocks = w ? gridDim.x - qblocks : qblocks;
+  const int heads = a.heads[w], d = a.d, half = a.rot / 2;
+  const long long rows = (long long)a.B * a.L * heads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T* gamma = static_cast<const T*>(a.gamma[w]);
+  constexpr int kPer = kMaxD / 32;
+  float sums[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) sums[k] = 0.f;
+  for (long long row = (long long)block * (kThreads / 32) + warp; row < rows;
+       row += (long long)blocks * (kThreads / 32)) {
+    const long long tok = row / heads;
+    const int h = (int)(row - tok * heads), b = (int)(tok / a.L), l = (int)(tok - (long long)b * a.L);
+    const long long arow = a.rot > 0 ? angle_row(a, b, l) : 0;
+    const T* xp = static_cast<const T*>(a.x[w].p) + a.x[w].at(b, l, h);
+    const T* yp = static_cast<const T*>(a.y[w].p) + a.y[w].at(b, l, h);
+    float x[kPer], part[kPer], ss = 0.f;  // own channel, and its partner's of the rotation
+    // the partner of channel c, its angle, and the sign of its sine term
+    auto pair = [&](int c, int* other, int* angle, float* sign) {
+      *angle = a.interleaved ? c >> 1 : (c < half ? c : c - half);
+      const bool first = a.interleaved ? (c & 1) == 0 : c < half;
+      *other = a.interleaved ? c ^ 1 : (first ? c + half : c - half);
+      *sign = first ? -1.f : 1.f;
+    };
+    float g[kPer], gpart[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int c = lane + 32 * k;
+      x[k] = part[k] = g[k] = gpart[k] = 0.f;
+      if (c >= d) continue;
+      x[k] = to_f(xp[c]);
+      ss = fmaf(x[k], x[k], ss);
+      int other = c, angle;
+      float sign;
+      if (c < a.rot) pair(c, &other, &angle, &sign);
+      part[k] = to_f(xp[other]);
+      if (kBackward) {
+        g[k] = to_f(yp[c]);
+        gpart[k] = to_f(yp[other]);
+      }
+    }
+    __syncwarp();  // every element is read before the row may be overwritten in place
+    const float r = rsqrtf(group_sum<32>(ss) / (float)d + a.eps);
+    float along = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int c = lane + 32 * k;
+      if (c >= d) continue;
+      int other = c, angle = 0;
+      float sign = 0.f, cs = 1.f, sn = 0.f;
+      if (c < a.rot) {
+        pair(c, &other, &angle, &sign);
+        cs = a.cosp[arow * half + angle];
+        sn = a.sinp[arow * half + angle];
+      }
+      if (!kBackward) {
+        const float n = x[k] * r * to_f(gamma[c]), m = part[k] * r * to_f(gamma[other]);
+        static_cast<T*>(a.y[w].p)[a.y[w].at(b, l, h) + c] = from_f<T>(n * cs + sign * m * sn);
+      } else {
+        const float gy = g[k] * cs - sign * gpart[k] * sn;
+        x[k] *= r;
+        sums[k] = fmaf(gy, x[k], sums[k]);
+        g[k] = gy * to_f(gamma[c]);
+        along = fmaf(g[k], x[k], along);
+      }
+    }
+    if (kBackward) {
+      along = group_sum<32>(along) / (float)d;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int c = lane + 32 * k;
+        if (c < d) static_cast<T*>(a.dx[w].p)[a.dx[w].at(b, l, h) + c] = from_f<T>(r * (g[k] - x[k] * along));
+      }
+    }
+  }
+  if (kBackward) {
+    __shared__ float s[kThreads / 32][kMaxD];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) s[warp][lane + 32 * k] = sums[k];
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < d; ch += kThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kThreads / 32; ++k) v += s[k][ch];
+      partial[(long long)blockIdx.x * d + ch] = v;
+    }
+  }
+}
+
+// dgamma = the blocks' shares added in a fixed order: 32 channels per block,
+// eight runs of blocks side by side.
+__global__ void __launch_bounds__(256) qk_norm_dgamma_kernel(QkNormArgs a, int qblocks, int blocks,
+                                                            const float* partial) {
+  __shared__ float s[8][33];
+  const int w = blockIdx.y, lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  const int lo = w ? qblocks : 0, hi = w ? blocks : qblocks;
+  float v = 0.f;
+  if (c < a.d)
+    for (int b = lo + run; b < hi; b += 8) v += partial[(long long)b * a.d + c];
+  s[run][lane] = v;
+  __syncthreads();
+  if (run == 0 && c < a.d) {
+    for (int k = 1; k < 8; ++k) v += s[k][lane];
+    a.dgamma[w][c] = v;
+  }
+}
+
+bool view_ok(const Heads& v, int esize) {
+  const long long m = 16 / esize;
+  return reinterpret_cast<uintptr_t>(v.p) % 16 == 0 && v.sb % m == 0 && v.st % m == 0 && v.sh % m == 0;
+}
+
+// The vector path needs rows and rotated parts of whole 16-channel pieces and
+// 16-byte aligned rows.
+bool vec_ok(const QkNormArgs& a, int esize, bool backward) {
+  if (a.d % 16 || a.rot % 16 || a.d > kMaxD) return false;
+  for (int w = 0; w < 2; ++w) {
+    if (!view_ok(a.x[w], esize) || !view_ok(a.y[w], esize) || (backward && !view_ok(a.dx[w], esize))) return false;
+    if (reinterpret_cast<uintptr_t>(a.gamma[w]) % 16) return false;
+  }
+  return a.rot == 0 || (reinterpret_cast<uintptr_t>(a.cosp) % 16 == 0 && reinterpret_cast<uintptr_t>(a.sinp) % 16 == 0);
+}
+
+int group_of(int d) {
+  int g = 1;
+  while (g < d / 16) g *= 2;
+  return g;
+}
+
+// Blocks of q and of k: enough rows in flight to fill the GPU (eight blocks of
+// 256 threads per SM), at most one step's rows per block when there are few.
+void grid_of(const QkNormArgs& a, int rows_per_block, int per_sm, int* q, int* k) {
+  const long long cap = (long long)sm_count() * per_sm;
+  const long long need[2] = {((long long)a.B * a.L * a.heads[0] + rows_per_block - 1) / rows_per_block,
+                             ((long long)a.B * a.L * a.heads[1] + rows_per_block - 1) / rows_per_block};
+  if (need[0] + need[1] <= cap) {
+    *q = (int)need[0];
+    *k = (int)need[1];
+    return;
+  }
+  long long nq = cap * a.heads[0] / (a.heads[0] + a.heads[1]);
+  nq = nq < 1 ? 1 : (nq > cap - 1 ? cap - 1 : nq);
+  *q = (int)(nq < need[0] ? nq : need[0]);
+  *k = (int)(cap - nq < need[1] ? cap - nq : need[1]);
+}
+
+template <class T, bool kBackward>
+void plan(const QkNormArgs& a, bool* vec, int* G, int* nq, int* nk) {
+  *vec = vec_ok(a, (int)sizeof(T), kBackward);
+  *G = *vec ? group_of(a.d) : 32;
+  grid_of(a, kThreads / *G, kBackward ? 4 : 8, nq, nk);
+}
+
+template <class T, bool kBackward>
+cudaError_t launch(const QkNormArgs& a, float* partial, cudaStream_t st) {
+  bool vec;
+  int G, nq, nk;
+  plan<T, kBackward>(a, &vec, &G, &nq, &nk);
+  const int grid = nq + nk;
+  prof_begin(kKindOther, st);
+  if (!vec)
+    qk_norm_any_kernel<T, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (G == 1)
+    qk_norm_vec_kernel<T, 1, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (G == 2)
+    qk_norm_vec_kernel<T, 2, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (G == 4)
+    qk_norm_vec_kernel<T, 4, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (G == 8)
+    qk_norm_vec_kernel<T, 8, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else
+    qk_norm_vec_kernel<T, 16, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  prof_end(kKindOther, st);
+  count_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !kBackward) return e;
+  prof_begin(kKindOther, st);
+  qk_norm_dgamma_kernel<<<dim3((a.d + 31) / 32, 2), 256, 0, st>>>(a, nq, grid, partial);
+  prof_end(kKindOther, st);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      n < 1)
+    return 1;
+  return n;
+}
+
+cudaError_t launch_qk_norm_forward(const QkNormArgs& a, int dtype, cudaStream_t st) {
+  if (dtype == kBF16) return launch<__nv_bfloat16, false>(a, nullptr, st);
+  if (dtype == kFP16) return launch<__half, false>(a, nullptr, st);
+  return launch<float, false>(a, nullptr, st);
+}
+
+size_t qk_norm_scratch_bytes(const QkNormArgs& a, int dtype) {
+  bool vec;
+  int G, nq, nk;
+  if (dtype == kF32)
+    plan<float, true>(a, &vec, &G, &nq, &nk);
+  else
+    plan<__half, true>(a, &vec, &G, &nq, &nk);
+  return (size_t)(nq + nk) * a.d * sizeof(float);
+}
+
+cudaError_t launch_qk_norm_backward(const QkNormArgs& a, int dtype, void* scratch, cudaStream_t st) {
+  float* partial = static_cast<float*>(scratch);
+  if (dtype == kBF16) return launch<__nv_bfloat16, true>(a, partial, st);
+  if (dtype == kFP16) return launch<__half, true>(a, partial, st);
+  return launch<float, true>(a, partial, st);
+}
+
+}  // namespace vswin

@@ -11,9 +11,8 @@
 #include <string>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/vswin.h"
+#include "api.h"
 #include "internal.h"
 
 namespace vswin {
@@ -40,18 +39,13 @@ bool take_injected(std::atomic<int>& pending) {
   return false;
 }
 
-// Names every entry call on the NVTX timeline (a no-op unless a tool listens).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
 const char* const kKindNames[kKinds] = {"vswin.qkv_gemm", "vswin.attention", "vswin.proj_gemm",
                                         "vswin.other",    "vswin.mlp",       "vswin.attention_bwd"};
 std::mutex g_mu;
 constexpr int kMaxDevices = 64;
 int* g_err_ptr[kMaxDevices] = {nullptr};
+
+}  // namespace
 
 int fail(int status, const char* fmt, ...) {
   char buf[512];
@@ -66,6 +60,8 @@ int fail(int status, const char* fmt, ...) {
 int fail_cuda(cudaError_t e, const char* what) {
   return fail(VSWIN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
+
+namespace {
 
 // Device address of the error word for the current device (looked up once per
 // device, with that device current).
@@ -85,6 +81,8 @@ int error_word(int** out) {
   return VSWIN_OK;
 }
 
+}  // namespace
+
 int make_ctx(KernelCtx* ctx) {
   if (take_injected(g_inject_cuda)) return fail(VSWIN_ERR_CUDA, "injected CUDA failure (test hook)");
   int* err = nullptr;
@@ -95,6 +93,8 @@ int make_ctx(KernelCtx* ctx) {
   ctx->force_exact = g_force_exact.load();
   return VSWIN_OK;
 }
+
+namespace {
 
 // Stream-ordered scratch comes from one library-owned memory pool per device
 // whose release threshold keeps freed blocks for the next call: without it
@@ -125,6 +125,8 @@ int scratch_pool(cudaMemPool_t* out) {
   return VSWIN_OK;
 }
 
+}  // namespace
+
 int scratch_alloc(void** p, size_t bytes, cudaStream_t st) {
   if (take_injected(g_inject_cuda)) return fail(VSWIN_ERR_CUDA, "injected CUDA failure (test hook)");
   if (take_injected(g_inject_alloc))
@@ -146,6 +148,8 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
   return pa < pb + nb && pb < pa + na;
 }
+
+namespace {
 
 int build_geom(int B, int T, int H, int W, int C, int heads, const int* window, const int* shift, Geom* g) {
   if (!window || !shift) return fail(VSWIN_ERR_INVALID_ARG, "window and shift must be non-NULL host arrays of 3");

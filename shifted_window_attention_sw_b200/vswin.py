@@ -46,6 +46,13 @@ EXPORTS = (
     "vswin_test_inject_failure",
     "vswin_debug_plant_row",
     "vswin_debug_bounds_enabled",
+    "vswin_qk_norm_forward",
+    "vswin_qk_norm_backward",
+    "vswin_bucket_map",
+    "vswin_bias_attention_forward",
+    "vswin_bias_attention_backward",
+    "vswin_adamw_step",
+    "vswin_adamw_decode",
 )
 
 KERNEL_KINDS = ("qkv_gemm", "attention", "proj_gemm", "other", "mlp", "attention_bwd")
@@ -61,6 +68,32 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _IP = ctypes.POINTER(ctypes.c_int)
+_LL = ctypes.c_longlong
+
+# vswin_dtype
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ADAMW_BLOCK = 256  # elements that share one scale of the 8-bit moments
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("batch_stride", _LL), ("token_stride", _LL), ("head_stride", _LL)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("cos", _P), ("sin", _P), ("rows", _I), ("dim", _I), ("interleaved", _I), ("positions", _P)]
+
+
+class _BucketBias(ctypes.Structure):
+    _fields_ = [("table", _P), ("map", _P), ("buckets", _I), ("max_distance", _I)]
+
+
+class _Visibility(ctypes.Structure):
+    _fields_ = [("q_lens", _P), ("kv_lens", _P), ("q_start", _P), ("causal", _I)]
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", _P), ("master", _P), ("grad", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P),
+                ("n", _LL), ("weight_decay", ctypes.c_double), ("param_dtype", _I), ("grad_dtype", _I)]
 
 
 def lib():
@@ -119,6 +152,20 @@ def lib():
         L.vswin_debug_plant_row.restype = _I
         L.vswin_debug_bounds_enabled.argtypes = []
         L.vswin_debug_bounds_enabled.restype = _I
+        H, D = ctypes.POINTER(_Heads), ctypes.c_double
+        norm = [_I] * 6 + [H, H, _P, _P, ctypes.c_float, ctypes.POINTER(_Rotation)]
+        attn = [_I] * 7 + [H, H, H, ctypes.c_float, ctypes.POINTER(_BucketBias), ctypes.POINTER(_Visibility)]
+        L.vswin_qk_norm_forward.argtypes = norm + [H, H, _P]
+        L.vswin_qk_norm_backward.argtypes = norm + [H, H, H, H, _P, _P, _P]
+        L.vswin_bucket_map.argtypes = [_I, _I, _I, _IP]
+        L.vswin_bias_attention_forward.argtypes = attn + [H, _P, _P]
+        L.vswin_bias_attention_backward.argtypes = attn + [H, _P, H, H, H, H, _P, _P]
+        L.vswin_adamw_step.argtypes = [ctypes.POINTER(_AdamwTensor), _I, _I, D, D, D, D, _LL, _P, _P, _P]
+        L.vswin_adamw_decode.argtypes = [_P, _P, _P, _P, _LL, _I, _P, _P, _P]
+        for name in ("vswin_qk_norm_forward", "vswin_qk_norm_backward", "vswin_bucket_map",
+                     "vswin_bias_attention_forward", "vswin_bias_attention_backward", "vswin_adamw_step",
+                     "vswin_adamw_decode"):
+            getattr(L, name).restype = _I
         _lib = L
     return _lib
 
@@ -373,6 +420,273 @@ def wmsa_forward_host(x_host, window, shift, Wqkv, bqkv, Wproj, bproj, table, he
     _check_shapes(x_host, window, heads, Wqkv, bqkv, Wproj, bproj, table, out_host=out_host)
     return _layer_call(lib().vswin_wmsa_forward_host, x_host, window, shift, Wqkv, bqkv, Wproj, bproj, table,
                        heads, out_host, stream, dev)
+
+
+# ------------------------------------------------------------------ token sequences
+def _heads(name, t, shape, dtype, device):
+    """View of a (B, L, heads, d) tensor; its channels have to be contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
+        raise ValueError(f"{name} must have contiguous channels, got strides {t.stride()}")
+    return _Heads(t.data_ptr(), sb, st, sh)
+
+
+def _flat(name, t, shape, dtype, device):
+    """Pointer of a contiguous tensor of a given shape and type, None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(q.shape)} and {tuple(k.shape)}")
+    if q.dtype not in DTYPES:
+        raise TypeError(f"q must be one of {list(DTYPES)}, got {q.dtype}")
+    B, L, hq, d = q.shape
+    hk, dt, dev = k.shape[2], q.dtype, q.device
+    rot = None
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2:
+            raise ValueError("cos and sin must both be (rows, dim / 2)")
+        shape = tuple(cos.shape)
+        rot = _Rotation(_flat("cos", cos, shape, torch.float32, dev), _flat("sin", sin, shape, torch.float32, dev),
+                        shape[0], 2 * shape[1], 1 if interleaved else 0,
+                        _flat("positions", positions, (B, L), torch.int32, dev))
+    elif positions is not None:
+        raise ValueError("positions need cos and sin")
+    views = (_heads("q", q, (B, L, hq, d), dt, dev), _heads("k", k, (B, L, hk, d), dt, dev))
+    return (B, L, hq, hk, d, dt, dev), [DTYPES[dt], B, L, hq, hk, d, *views,
+                                        _flat("gamma_q", gamma_q, (d,), dt, dev),
+                                        _flat("gamma_k", gamma_k, (d,), dt, dev), float(eps), rot]
+
+
+def qk_norm_forward(q, k, gamma_q, gamma_k, eps=1e-6, cos=None, sin=None, positions=None, interleaved=False,
+                    q_out=None, k_out=None, stream=None):
+    """Norm of every head of q (B, L, hq, d) and k (B, L, hk, d) over its d channels, times gamma [d], then
+    the rotation of the first 2 * cos.shape[1] channels by row ``positions[b, l]`` (int32; row l without
+    them) of the float32 tables cos and sin, in one pass; bf16, fp16 or fp32. Views with contiguous channels
+    are taken as they are. ``q_out`` may be ``q`` and ``k_out`` ``k``. Returns (q_out, k_out)."""
+    (B, L, hq, hk, d, dt, dev), args = _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
+    q_out = torch.empty((B, L, hq, d), dtype=dt, device=dev) if q_out is None else q_out
+    k_out = torch.empty((B, L, hk, d), dtype=dt, device=dev) if k_out is None else k_out
+    with torch.cuda.device(dev):
+        _check(lib().vswin_qk_norm_forward(*args, _heads("q_out", q_out, (B, L, hq, d), dt, dev),
+                                           _heads("k_out", k_out, (B, L, hk, d), dt, dev), _stream_handle(stream, dev)))
+    return q_out, k_out
+
+
+def qk_norm_backward(q, k, gamma_q, gamma_k, dq_out, dk_out, eps=1e-6, cos=None, sin=None, positions=None,
+                     interleaved=False, dq=None, dk=None, stream=None):
+    """Gradients (dq, dk in the type of q; dgamma_q, dgamma_k float32) of qk_norm_forward for the output
+    gradients ``dq_out`` and ``dk_out``. ``dq`` and ``dk`` may be given, e.g. as slices of one buffer."""
+    (B, L, hq, hk, d, dt, dev), args = _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
+    dq = torch.empty((B, L, hq, d), dtype=dt, device=dev) if dq is None else dq
+    dk = torch.empty((B, L, hk, d), dtype=dt, device=dev) if dk is None else dk
+    dgamma = torch.empty((2, d), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().vswin_qk_norm_backward(
+            *args, _heads("dq_out", dq_out, (B, L, hq, d), dt, dev), _heads("dk_out", dk_out, (B, L, hk, d), dt, dev),
+            _heads("dq", dq, (B, L, hq, d), dt, dev), _heads("dk", dk, (B, L, hk, d), dt, dev),
+            dgamma[0].data_ptr(), dgamma[1].data_ptr(), _stream_handle(stream, dev)))
+    return dq, dk, dgamma[0], dgamma[1]
+
+
+def bucket_map(buckets, max_distance, bidirectional=True, device="cuda"):
+    """int32 tensor [2 * max_distance + 1]: the bucket of each offset key - query in [-max_distance,
+    max_distance] (see vswin_bucket_map), as the attention with bucketed bias takes it."""
+    out = torch.empty(2 * max(int(max_distance), 0) + 1, dtype=torch.int32)
+    _check(lib().vswin_bucket_map(int(buckets), int(max_distance), 1 if bidirectional else 0,
+                                  ctypes.cast(out.data_ptr(), _IP)))
+    return out.to(device)
+
+
+def _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens, kv_lens, q_start):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(q.shape)} and {tuple(k.shape)}")
+    if q.dtype not in DTYPES:
+        raise TypeError(f"q must be torch.bfloat16 or torch.float16, got {q.dtype}")
+    B, Lq, hq, d = q.shape
+    Lk, hk = k.shape[1:3]
+    dt, dev = q.dtype, q.device
+    if table.dim() != 2 or bucket_map.dim() != 1 or bucket_map.shape[0] % 2 == 0:
+        raise ValueError("table must be (buckets, heads of q) and bucket_map (2 * max_distance + 1,), got "
+                         f"{tuple(table.shape)} and {tuple(bucket_map.shape)}")
+    buckets, D = table.shape[0], bucket_map.shape[0] // 2
+    views = (_heads("q", q, (B, Lq, hq, d), dt, dev), _heads("k", k, (B, Lk, hk, d), dt, dev),
+             _heads("v", v, (B, Lk, hk, d), dt, dev))
+    bias = _BucketBias(_flat("table", table, (buckets, hq), dt, dev),
+                       _flat("bucket_map", bucket_map, (2 * D + 1,), torch.int32, dev), buckets, D)
+    vis = _Visibility(_flat("q_lens", q_lens, (B,), torch.int32, dev), _flat("kv_lens", kv_lens, (B,), torch.int32, dev),
+                      _flat("q_start", q_start, (B,), torch.int32, dev), 1 if causal else 0)
+    scale = d ** -0.5 if scale is None else float(scale)
+    return (B, Lq, Lk, hq, hk, d, dt, dev), [DTYPES[dt], B, Lq, Lk, hq, hk, d, *views, scale, bias, vis]
+
+
+def bias_attention_forward(q, k, v, table, bucket_map, scale=None, causal=False, q_lens=None, kv_lens=None,
+                           q_start=None, out=None, lse=None, stream=None):
+    """Attention of q (B, Lq, hq, d) over k, v (B, Lk, hk, d) with the bias table[bucket_map[key - position]][head];
+    bf16 or fp16, d 32, 64 or 128, hq a multiple of hk. Query i of sequence b stands at position q_start[b] + i;
+    it sees the keys below kv_lens[b] (with ``causal`` up to its own position), rows from q_lens[b] on are zero
+    (int32 tensors [B], default: all). ``scale`` defaults to d ** -0.5. One new token of each sequence against a
+    cache: Lq = 1, q_start = kv_lens - 1. Returns (out, lse), lse float32 (B, hq, Lq)."""
+    (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
+                                                                 kv_lens, q_start)
+    out = torch.empty((B, Lq, hq, d), dtype=dt, device=dev) if out is None else out
+    lse = torch.empty((B, hq, Lq), dtype=torch.float32, device=dev) if lse is None else lse
+    with torch.cuda.device(dev):
+        _check(lib().vswin_bias_attention_forward(*args, _heads("out", out, (B, Lq, hq, d), dt, dev),
+                                                  _flat("lse", lse, (B, hq, Lq), torch.float32, dev),
+                                                  _stream_handle(stream, dev)))
+    return out, lse
+
+
+def bias_attention_backward(q, k, v, table, bucket_map, out, lse, dout, scale=None, causal=False, q_lens=None,
+                            kv_lens=None, q_start=None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv, dtable, all in the type of q) of bias_attention_forward for the output gradient
+    ``dout``, from its ``out`` and ``lse``. ``dq``, ``dk`` and ``dv`` may be given, e.g. as slices of one buffer."""
+    (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
+                                                                 kv_lens, q_start)
+    qs, ks = (B, Lq, hq, d), (B, Lk, hk, d)
+    dq, dk, dv = (torch.empty(s, dtype=dt, device=dev) if t is None else t for t, s in ((dq, qs), (dk, ks), (dv, ks)))
+    dtable = torch.empty_like(table)
+    with torch.cuda.device(dev):
+        _check(lib().vswin_bias_attention_backward(
+            *args, _heads("out", out, qs, dt, dev), _flat("lse", lse, (B, hq, Lq), torch.float32, dev),
+            _heads("dout", dout, qs, dt, dev), _heads("dq", dq, qs, dt, dev), _heads("dk", dk, ks, dt, dev),
+            _heads("dv", dv, ks, dt, dev), dtable.data_ptr(), _stream_handle(stream, dev)))
+    return dq, dk, dv, dtable
+
+
+# ------------------------------------------------------------------ optimizer
+class AdamW:
+    """AdamW over a list of contiguous weights on one CUDA device (see vswin_adamw_step): every step is one
+    launch per 192 tensors. The object owns the moments (zeros, or the ones given) and keeps the weights' list.
+
+    weight_decay: one value or one per weight. bits: 32 (float32 moments) or 8 (codes with a scale per 256
+    elements). master: float32 copies that are stepped and rounded into the weights: True makes them, or a list.
+    moments: (m, v) lists to go on from, with ``scales`` (m_scale, v_scale) for 8 bits."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, master=None,
+                 moments=None, scales=None):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        if bits not in (8, 32):
+            raise ValueError(f"bits must be 32 or 8, got {bits}")
+        self.lr, self.betas, self.eps, self.bits, self.steps = lr, tuple(betas), eps, bits, 0
+        dev = self.device = self.params[0].device
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(self.params)
+        if len(decay) != len(self.params):
+            raise ValueError(f"{len(decay)} weight decays for {len(self.params)} parameters")
+        if moments is None and scales is not None:
+            raise ValueError("scales need moments")
+        if moments is not None and bits == 8 and scales is None:
+            raise ValueError("8-bit moments need their scales")
+
+        def state(given, which, dtype, shape_of):
+            if given is not None:
+                return self._list(f"{which}", given[0 if which.startswith("m") else 1])
+            return [torch.zeros(shape_of(p), dtype=dtype, device=dev) for p in self.params]
+
+        full = lambda p: tuple(p.shape)  # noqa: E731
+        blocks = lambda p: (-(-p.numel() // ADAMW_BLOCK),)  # noqa: E731
+        mt, vt = (torch.float32, torch.float32) if bits == 32 else (torch.int8, torch.uint8)
+        self.m, self.v = state(moments, "m", mt, full), state(moments, "v", vt, full)
+        scales = scales if bits == 8 else None
+        self.m_scale = state(scales, "m_scale", torch.float32, blocks) if bits == 8 else None
+        self.v_scale = state(scales, "v_scale", torch.float32, blocks) if bits == 8 else None
+        if master is True:
+            master = [p.detach().float() for p in self.params]
+            master = [t.clone() if t.data_ptr() == p.data_ptr() else t for t, p in zip(master, self.params)]
+        self.master = None if not master else self._list("master", master)
+        self._records = (_AdamwTensor * len(self.params))()
+        for i, (p, r) in enumerate(zip(self.params, self._records)):
+            if p.dtype not in DTYPES:
+                raise TypeError(f"params[{i}] must be one of {list(DTYPES)}, got {p.dtype}")
+            r.param = _flat(f"params[{i}]", p, full(p), p.dtype, dev)
+            r.m = _flat(f"m[{i}]", self.m[i], full(p), mt, dev)
+            r.v = _flat(f"v[{i}]", self.v[i], full(p), vt, dev)
+            if bits == 8:
+                r.m_scale = _flat(f"m_scale[{i}]", self.m_scale[i], blocks(p), torch.float32, dev)
+                r.v_scale = _flat(f"v_scale[{i}]", self.v_scale[i], blocks(p), torch.float32, dev)
+            if self.master:
+                r.master = _flat(f"master[{i}]", self.master[i], full(p), torch.float32, dev)
+            r.n, r.weight_decay, r.param_dtype = p.numel(), decay[i], DTYPES[p.dtype]
+        self._shapes = [p.shape for p in self.params]
+
+    def _list(self, name, tensors):
+        tensors = list(tensors)
+        if len(tensors) != len(self.params):
+            raise ValueError(f"{name}: {len(tensors)} tensors for {len(self.params)} parameters")
+        return tensors
+
+    def step(self, grads, lr=None, step=None, grad_scale=None, stream=None):
+        """One step with ``grads`` (contiguous, shaped as the weights; bf16, fp16 or fp32). ``step`` counts from 1
+        (default: one more than the last) or is a one-element int32 CUDA tensor, read when the step runs, as a
+        captured step needs. grad_scale: one-element float32 CUDA tensor that multiplies every gradient."""
+        grads = self._list("grads", grads)
+        dev = self.device
+        for i, (g, r, shape) in enumerate(zip(grads, self._records, self._shapes)):
+            dt = DTYPES.get(g.dtype)
+            if dt is None or g.shape != shape or g.device != dev or not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be a contiguous {tuple(shape)} tensor of {list(DTYPES)} on {dev}, "
+                                 f"got {g.dtype} {tuple(g.shape)} on {g.device}")
+            r.grad = g.data_ptr()
+            r.grad_dtype = dt
+        count, count_dev = self.steps + 1, None
+        if isinstance(step, torch.Tensor):
+            count_dev = _flat("step", step, tuple(step.shape), torch.int32, dev)
+            if step.numel() != 1:
+                raise ValueError("step must have one element")
+        elif step is not None:
+            count = int(step)
+        if grad_scale is not None and grad_scale.numel() != 1:
+            raise ValueError("grad_scale must have one element")
+        gs = None if grad_scale is None else _flat("grad_scale", grad_scale, tuple(grad_scale.shape), torch.float32, dev)
+        with torch.cuda.device(dev):
+            _check(lib().vswin_adamw_step(self._records, len(self._records), self.bits,
+                                          float(self.lr if lr is None else lr), *map(float, self.betas),
+                                          float(self.eps), count, count_dev, gs, _stream_handle(stream, dev)))
+        self.steps = count
+        return self
+
+    def moments(self, dtype=torch.float32, stream=None):
+        """(m, v) lists of the moments' values: the states themselves for 32 bits, decoded copies for 8."""
+        if self.bits == 32:
+            return self.m, self.v
+        pairs = [adamw_decode(*t, dtype=dtype, stream=stream)
+                 for t in zip(self.m, self.m_scale, self.v, self.v_scale)]
+        return [a for a, _ in pairs], [b for _, b in pairs]
+
+
+def adamw_decode(m, m_scale, v, v_scale, dtype=torch.float32, stream=None):
+    """(m, v) that 8-bit moments stand for: codes int8 and uint8 of one shape, scales float32 per 256 elements."""
+    dev, shape = m.device, tuple(m.shape)
+    if dtype not in DTYPES:
+        raise TypeError(f"dtype must be one of {list(DTYPES)}, got {dtype}")
+    blocks = (-(-m.numel() // ADAMW_BLOCK),)
+    args = (_flat("m", m, shape, torch.int8, dev), _flat("m_scale", m_scale, blocks, torch.float32, dev),
+            _flat("v", v, shape, torch.uint8, dev), _flat("v_scale", v_scale, blocks, torch.float32, dev))
+    mo, vo = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().vswin_adamw_decode(*args, m.numel(), DTYPES[dtype], mo.data_ptr(), vo.data_ptr(),
+                                        _stream_handle(stream, dev)))
+    return mo, vo
 
 
 def index_maps(B, T, H, W, window, shift, device="cuda", stream=None):

@@ -1,0 +1,240 @@
+"""The operators over token sequences and the optimizer step on the host: refusals before any launch, the bucket
+map, and the float64 definitions against central differences. CPU only."""
+
+import ctypes
+import math
+from fractions import Fraction
+
+import pytest
+import torch
+
+import sequence_reference as ref
+from shifted_window_attention_sw_b200 import build as build_mod
+from shifted_window_attention_sw_b200 import vswin
+
+
+@pytest.fixture(scope="module")
+def L():
+    build_mod.build()
+    return vswin.lib()
+
+
+# fake device pointers, 16 MB apart: never dereferenced, because validation fails first
+def P(n, off=0):
+    return (n << 24) + off
+
+
+def _view(n, L, H, d, off=0, **kw):
+    s = dict(batch_stride=L * H * d, token_stride=H * d, head_stride=d)
+    s.update(kw)
+    return vswin._Heads(P(n, off) if n else None, s["batch_stride"], s["token_stride"], s["head_stride"])
+
+
+def _norm(L, dtype=0, B=2, Lt=8, hq=4, hk=2, d=64, q=None, k=None, gq=3, gk=4, eps=1e-6, rot=None, qo=None, ko=None,
+          back=None):
+    q = _view(1, Lt, max(hq, 1), d) if q is None else q
+    k = _view(2, Lt, max(hk, 1), d) if k is None else k
+    qo = _view(5, Lt, max(hq, 1), d) if qo is None else qo
+    ko = _view(6, Lt, max(hk, 1), d) if ko is None else ko
+    args = [dtype, B, Lt, hq, hk, d, q, k, P(gq) if gq else None, P(gk) if gk else None, eps, rot, qo, ko]
+    if back is None:
+        return L.vswin_qk_norm_forward(*args, None)
+    b = dict(dq=_view(7, Lt, hq, d), dk=_view(8, Lt, hk, d), g=P(9), h=P(10))
+    b.update(back)
+    return L.vswin_qk_norm_backward(*args, b["dq"], b["dk"], b["g"], b["h"], None)
+
+
+def _refused(L, rc, status=vswin.ERR_INVALID_ARG, before=None):
+    assert rc == status, (rc, vswin.last_error())
+    assert vswin.last_error()
+    assert vswin.launch_count() == before
+
+
+def _rot(rows=8, dim=32, cos=11, sin=12, positions=None, inter=0):
+    return vswin._Rotation(P(cos) if cos else None, P(sin) if sin else None, rows, dim, inter, positions)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype=3), dict(dtype=-1), dict(B=0), dict(Lt=0), dict(hq=0), dict(hk=-1), dict(d=0), dict(eps=-1.0),
+    dict(eps=math.inf), dict(eps=math.nan), dict(gq=0), dict(gk=0), dict(q=_view(0, 8, 4, 64)),
+    dict(q=_view(1, 8, 4, 64, off=1)), dict(q=_view(1, 8, 4, 64, token_stride=-4)),
+    dict(qo=_view(5, 8, 4, 64, token_stride=0)), dict(qo=_view(5, 8, 4, 64, head_stride=32)),
+    dict(qo=_view(1, 8, 4, 64, off=64)), dict(qo=_view(2, 8, 4, 64)), dict(ko=_view(5, 8, 2, 64)),
+    dict(rot=_rot(dim=33)), dict(rot=_rot(dim=66)), dict(rot=_rot(dim=-2)), dict(rot=_rot(cos=0)), dict(rot=_rot(sin=0)),
+    dict(rot=_rot(rows=0)), dict(rot=_rot(rows=7)), dict(rot=_rot(positions=P(13, 2))),
+    dict(back=dict(g=None)), dict(back=dict(g=P(10))), dict(back=dict(h=P(1, 64))), dict(back=dict(dq=_view(2, 8, 4, 64))),
+    dict(back=dict(dq=_view(7, 8, 4, 64, batch_stride=64))), dict(back=dict(dk=_view(7, 8, 2, 64))),
+], ids=str)
+def test_norm_refusals(L, kw):
+    before = vswin.launch_count()
+    _refused(L, _norm(L, **kw), before=before)
+
+
+def test_norm_unsupported_width(L):
+    before = vswin.launch_count()
+    _refused(L, _norm(L, d=257), vswin.ERR_UNSUPPORTED, before)
+
+
+def _attn(L, dtype=0, B=2, Lq=8, Lk=8, hq=4, hk=2, d=64, q=None, k=None, v=None, scale=0.125, table=4, bmap=5, buckets=32,
+          D=128, vis=None, out=None, lse=7, back=None):
+    q = _view(1, Lq, max(hq, 1), d) if q is None else q
+    k = _view(2, Lk, max(hk, 1), d) if k is None else k
+    v = _view(3, Lk, max(hk, 1), d) if v is None else v
+    out = _view(6, Lq, max(hq, 1), d) if out is None else out
+    bias = vswin._BucketBias(P(table) if table else None, P(bmap) if bmap else None, buckets, D)
+    args = [dtype, B, Lq, Lk, hq, hk, d, q, k, v, scale, bias, vis, out, P(lse) if lse else None]
+    if back is None:
+        return L.vswin_bias_attention_forward(*args, None)
+    b = dict(do=_view(8, Lq, hq, d), dq=_view(9, Lq, hq, d), dk=_view(10, Lk, hk, d), dv=_view(11, Lk, hk, d), dt=P(12))
+    b.update(back)
+    return L.vswin_bias_attention_backward(*args, b["do"], b["dq"], b["dk"], b["dv"], b["dt"], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype=5), dict(B=0), dict(Lq=0), dict(Lk=0), dict(hq=0), dict(hk=0), dict(d=0), dict(hq=3), dict(scale=math.nan),
+    dict(scale=math.inf), dict(table=0), dict(bmap=0), dict(buckets=0), dict(buckets=4097), dict(D=-1), dict(D=2**20 + 1),
+    dict(lse=0), dict(q=_view(1, 8, 4, 64, off=8)), dict(k=_view(2, 8, 2, 64, token_stride=132)),
+    dict(v=_view(0, 8, 2, 64)), dict(out=_view(1, 8, 4, 64)), dict(out=_view(2, 8, 4, 64, off=256)),
+    dict(out=_view(6, 8, 4, 64, head_stride=0)), dict(lse=6), dict(lse=1),
+    dict(vis=vswin._Visibility(P(13, 2), None, None, 0)), dict(vis=vswin._Visibility(None, P(13, 1), None, 0)),
+    dict(vis=vswin._Visibility(None, None, P(13, 3), 1)),
+    dict(back=dict(dt=None)), dict(back=dict(dt=P(9))), dict(back=dict(dt=P(4))), dict(back=dict(dq=_view(1, 8, 4, 64))),
+    dict(back=dict(dk=_view(8, 8, 2, 64))), dict(back=dict(dk=_view(9, 8, 2, 64))), dict(back=dict(dv=_view(10, 8, 2, 64))),
+    dict(back=dict(dv=_view(11, 8, 2, 64, token_stride=64))), dict(back=dict(do=_view(8, 8, 4, 64, off=2))),
+], ids=str)
+def test_attention_refusals(L, kw):
+    before = vswin.launch_count()
+    _refused(L, _attn(L, **kw), before=before)
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=2), dict(d=48), dict(d=256), dict(Lk=2**28 + 1), dict(hq=8192, hk=8192)], ids=str)
+def test_attention_unsupported(L, kw):
+    before = vswin.launch_count()
+    _refused(L, _attn(L, **kw), vswin.ERR_UNSUPPORTED, before)
+
+
+def _adam(L, bits=32, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, step=1, count=1, step_dev=None, gs=None, **kw):
+    f = dict(param=P(1), master=None, grad=P(2), m=P(3), v=P(4), m_scale=P(5), v_scale=P(6), n=1000, weight_decay=0.1,
+             param_dtype=0, grad_dtype=2)
+    f.update(kw)
+    t = (vswin._AdamwTensor * 1)(vswin._AdamwTensor(*(f[n] for n, _ in vswin._AdamwTensor._fields_)))
+    return L.vswin_adamw_step(t if count else None, abs(count), bits, lr, b1, b2, eps, step, step_dev, gs, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(bits=16), dict(lr=-1.0), dict(lr=math.inf), dict(b1=1.0), dict(b2=-0.1), dict(eps=-1.0), dict(step=0),
+    dict(step_dev=P(9, 1)), dict(gs=P(9, 2)), dict(n=-1), dict(param_dtype=3), dict(grad_dtype=-1), dict(param=None),
+    dict(grad=None), dict(m=None), dict(v=P(4, 2)), dict(master=P(7, 2)), dict(master=P(1)), dict(grad=P(1, 16)), dict(m=P(4)),
+    dict(bits=8, m_scale=None), dict(bits=8, v_scale=P(6, 1)), dict(bits=8, v_scale=P(5)), dict(weight_decay=math.nan),
+    dict(weight_decay=-0.1),
+], ids=str)
+def test_adamw_refusals(L, kw):
+    before = vswin.launch_count()
+    _refused(L, _adam(L, **kw), before=before)
+
+
+def test_decode_refusals(L):
+    before = vswin.launch_count()
+    args = [P(1), P(2), P(3), P(4), 100, 2, P(5), P(6), None]
+    for at, v in ((0, None), (1, P(2, 1)), (3, None), (4, -1), (5, 7), (6, P(1)), (7, P(5)), (7, P(6, 2))):
+        _refused(L, L.vswin_adamw_decode(*args[:at], v, *args[at + 1:]), before=before)
+
+
+def test_binding_refuses_before_the_library(L):
+    x = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    w, t, m = x[0, 0, 0], torch.zeros(32, 2, dtype=torch.bfloat16), vswin.bucket_map(32, 128, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        vswin.qk_norm_forward(x, x, w, w)
+    with pytest.raises(ValueError, match="CUDA"):
+        vswin.bias_attention_forward(x, x, x, t, m)
+    with pytest.raises(TypeError):
+        vswin.qk_norm_forward(x.double(), x, w, w)
+    with pytest.raises(ValueError):
+        vswin.qk_norm_forward(x[0], x, w, w)
+    with pytest.raises(ValueError):
+        vswin.bias_attention_forward(x, x, x, t, m[:-1])
+    with pytest.raises(ValueError):
+        vswin.AdamW([])
+    with pytest.raises(ValueError, match="CUDA"):
+        vswin.AdamW([w])
+
+
+# ------------------------------------------------------------------ bucket map
+def _exact_bucket(rel, buckets, D, bidirectional):
+    side = buckets // 2 if bidirectional else buckets
+    near = side // 2
+    n = abs(rel) if bidirectional else max(-rel, 0)
+    b = n
+    if n >= near:
+        m, t = side - near, 0
+        # largest t < m with (n / near)^m >= (D / near)^t, in whole numbers
+        while t + 1 < m and Fraction(n, near) ** m >= Fraction(D, near) ** (t + 1):
+            t += 1
+        b = near + t
+    return b + (side if bidirectional and rel > 0 else 0)
+
+
+@pytest.mark.parametrize("buckets,D,bidirectional", [(32, 128, True), (32, 128, False), (8, 16, True), (2, 5, False),
+                                                     (64, 512, True), (10, 81, False), (4, 2, True)], ids=str)
+def test_bucket_map(L, buckets, D, bidirectional):
+    got = vswin.bucket_map(buckets, D, bidirectional, device="cpu").tolist()
+    assert got == [_exact_bucket(r, buckets, D, bidirectional) for r in range(-D, D + 1)]
+
+
+@pytest.mark.parametrize("args", [(1, 128, True), (0, 128, False), (31, 128, True), (32, 8, True), (32, 2**20 + 1, True)])
+def test_bucket_map_refusals(L, args):
+    with pytest.raises(vswin.VswinError) as e:
+        vswin.bucket_map(*args, device="cpu")
+    assert e.value.status == vswin.ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ definitions against differences
+def _along(f, xs, us, h=1e-5):
+    """Central difference of the scalar f along the directions us."""
+    return (f(*[x + h * u for x, u in zip(xs, us)]) - f(*[x - h * u for x, u in zip(xs, us)])) / (2 * h)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_definition(interleaved):
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    x, w, dy, a = r(2, 3, 2, 10), r(10), r(2, 3, 2, 10), r(5, 3)
+    pos = torch.tensor([[0, 4, 2], [1, 1, 3]])
+    kw = dict(eps=1e-3, cos=a.cos(), sin=a.sin(), positions=pos, interleaved=interleaved)
+    res = ref.qk_norm(x, w, dy=dy, **kw)
+    ux, uw = r(*x.shape), r(*w.shape)
+    num = _along(lambda x, w: (ref.qk_norm(x, w, **kw)["y"] * dy).sum(), (x, w), (ux, uw))
+    assert abs(num - (res["dx"] * ux).sum() - (res["dgamma"] * uw).sum()) < 1e-7 * (1 + abs(num))
+
+
+def test_attention_definition():
+    g = torch.Generator().manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    q, k, v, do, t = r(2, 5, 4, 8), r(2, 7, 2, 8), r(2, 7, 2, 8), r(2, 5, 4, 8), r(6, 4)
+    t[2, 1] = -math.inf
+    m = torch.randint(0, 6, (7,), generator=g)
+    kw = dict(causal=True, q_lens=[5, 3], kv_lens=[6, 7], q_start=[2, -1])
+    res = ref.bias_attention(q, k, v, t, m, 0.3, dout=do, **kw)
+    us = [r(*x.shape) for x in (q, k, v, t)]
+    num = _along(lambda q, k, v, t: (ref.bias_attention(q, k, v, t, m, 0.3, **kw)["out"] * do).sum(), (q, k, v, t), us)
+    got = sum((res[n] * u).sum() for n, u in zip(("dq", "dk", "dv", "dtable"), us))
+    assert abs(num - got) < 1e-6 * (1 + abs(num))
+    assert res["lse"][1, :, 0].eq(-math.inf).all() and res["out"][1, 0].eq(0).all()
+
+
+def test_adamw_definition():
+    g = torch.Generator().manual_seed(3)
+    p = torch.randn(50, generator=g, dtype=torch.float64, requires_grad=True)
+    opt = torch.optim.AdamW([p], lr=1e-2, betas=(0.8, 0.95), eps=1e-6, weight_decay=0.3)
+    w, m, v = p.detach().clone(), torch.zeros(50).double(), torch.zeros(50).double()
+    for step in (1, 2, 3):
+        p.grad = torch.randn(50, generator=g, dtype=torch.float64)
+        w, m, v = ref.adamw(w, p.grad, m, v, 1e-2, 0.8, 0.95, 1e-6, 0.3, step)
+        opt.step()
+        assert torch.allclose(w, p.detach(), rtol=1e-12, atol=1e-14)
+
+
+def test_ctypes_records_match_the_header():
+    assert ctypes.sizeof(vswin._Heads) == 32 and ctypes.sizeof(vswin._Rotation) == 40
+    assert ctypes.sizeof(vswin._BucketBias) == 24 and ctypes.sizeof(vswin._Visibility) == 32
+    assert ctypes.sizeof(vswin._AdamwTensor) == 80
