@@ -1,14 +1,27 @@
 // What the kernels of the attention with bucketed bias share: the lengths and
-// positions of a sequence and the bias of an offset.
+// positions of a sequence, the bias of an offset, and the tensor-core tiles.
+//
+// Tiles in shared memory: rows of D channels as 8 x 16-byte core matrices
+// without swizzle, element (row r, channel c) at (r / 8) 16 D + (c / 8) 128 +
+// (r % 8) 16 + (c % 8) 2. The same tile serves as a K-major operand (rows are
+// M or N, channels are K: 128 bytes between 8-channel groups, 16 D between
+// 8-row groups) and as an MN-major one (channels are N, rows are K).
 #pragma once
 
+#include <cmath>
+
 #include "sequence.h"
+#include "sm100.cuh"
 
 namespace vswin {
 
 // A bias at or below this takes its key out of the softmax, as -inf does (so
 // that the lowest value of a type works as a mask).
 constexpr float kExclude = -1e30f;
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum : int { kErrAttnLoad = 0x121, kErrAttnMma = 0x122, kErrAttnSoftmax = 0x123 };
 
 struct SeqLens {
   int nq, nk;  // query rows and keys that take part
@@ -47,6 +60,128 @@ __device__ __forceinline__ float bias_of(const BiasAttnArgs& a, int rel, int h, 
   if (bucket) *bucket = k;
   const float v = to_f(static_cast<const T*>(a.table)[(long long)k * a.hq + h]);
   return v <= kExclude ? -INFINITY : v;
+}
+
+// The same in units of log2, with the causal rule (a key behind the query's
+// position is taken out) folded in.
+template <class T>
+__device__ __forceinline__ float bias2_of(const BiasAttnArgs& a, int rel, int h) {
+  const float v = bias_of<T>(a, rel, h) * kLog2E;
+  return a.causal && rel > 0 ? -INFINITY : v;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Instruction descriptor of an MMA on T (both operands) with fp32 accumulation.
+template <class T>
+__host__ __device__ constexpr uint32_t idesc16(int M, int N, int a_mn, int b_mn) {
+  return sizeof(T) == 2 && std::is_same<T, __half>::value
+             ? idesc_bf16(M, N, a_mn, b_mn) & ~((7u << 7) | (7u << 10))  // format 0: fp16
+             : idesc_bf16(M, N, a_mn, b_mn);
+}
+
+// Operand descriptors of a tile of D channels starting at `addr`.
+template <int D>
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {  // channels are K; 16 channels = +256 bytes
+  return smem_desc(addr, 128, 16 * D);
+}
+template <int D>
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {  // rows are K; 16 rows = +32 D bytes
+  return smem_desc(addr, 16 * D, 128);
+}
+
+// D[128 x N] (+)= A B^T, both tiles K-major over D channels.
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr, uint32_t idesc) {
+  const uint64_t da = desc_k<D>(a_addr), db = desc_k<D>(b_addr);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) umma_ss(d_tmem, da + 16 * k, db + 16 * k, idesc, k > 0);
+}
+// D[128 x D] (+)= A[128 x ROWS] B, A packed in TMEM (8 columns per 16 rows of B), B a tile of ROWS rows.
+template <int D, int ROWS>
+__device__ __forceinline__ void mma_acc(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_addr, uint32_t idesc, bool first) {
+  const uint64_t db = desc_mn<D>(b_addr);
+#pragma unroll
+  for (int k = 0; k < ROWS / 16; ++k)
+    umma_ts(d_tmem, a_tmem + 8 * k, db + (uint64_t)(2 * D * k), idesc, (first && k == 0) ? 0u : 1u);
+}
+
+// cp.async of rows [r0, r0 + ROWS) of a head into a tile; rows outside [0, n)
+// become zeros. `p` of `threads` threads (whole warps); a warp's copy takes 8
+// rows of 4 pieces of 16 bytes (64 contiguous bytes of a row, 128 contiguous
+// bytes of shared memory per 8 lanes).
+template <class T, int D, int ROWS, int THREADS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const T* head, long long row_stride, int r0, int n, int p) {
+  const int r = p & 7, c = (p >> 3) & 3;
+  constexpr int kGroups = ROWS / 8 * (D / 32);  // groups of 8 rows x 32 channels
+#pragma unroll
+  for (int g = 0; g < kGroups; g += THREADS / 32) {
+    const int gi = g + (p >> 5);
+    if (kGroups % (THREADS / 32) != 0 && gi >= kGroups) break;
+    const int rg = gi / (D / 32), cg = gi % (D / 32);
+    const int row = r0 + rg * 8 + r;
+    const bool in = row >= 0 && row < n;
+    const T* src = head + (in ? (long long)row * row_stride : 0) + cg * 32 + c * 8;
+    const uint32_t to = dst + rg * 16 * D + (cg * 4 + c) * 128 + r * 16;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(in ? 16u : 0u) : "memory");
+  }
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A whole warp waits; false in every lane when any lane's wait gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtx& ctx, int code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx.err, code, ctx.wait_limit));
+}
+
+// The bias of a 128 x BN tile as one line: entry t holds the offset base + t -
+// 127, so that row i and column j read entry j - i + 127. Written by `THREADS`
+// threads; `same` of each of their warps says whether all its entries equal
+// `value` (far tiles have one bucket: their rows read no line at all).
+template <int BN>
+struct BiasLine {
+  float line[128 + BN];
+  float value;
+  int same[4];
+};
+template <class T, int BN, int THREADS>
+__device__ __forceinline__ void fill_bias_line(BiasLine<BN>* o, const BiasAttnArgs& a, int h, int base, int p) {
+  const float first = bias2_of<T>(a, base, h);
+  bool same = true;
+  // a tile beyond the map's ends, on one side of the causal border
+  const bool far = base - 127 >= a.D + 1 || base + BN - 1 <= -a.D;
+  if (!far) {
+#pragma unroll
+    for (int t = 0; t < 127 + BN; t += THREADS) {
+      if (t + p < 127 + BN) {
+        const float v = bias2_of<T>(a, base + t + p - 127, h);
+        o->line[t + p] = v;
+        same = same && v == first;
+      }
+    }
+  }
+  same = __all_sync(0xffffffffu, same);
+  if ((p & 31) == 0) o->same[p >> 5] = same;
+  if (p == 0) o->value = first;
 }
 
 }  // namespace vswin
