@@ -44,12 +44,13 @@ constexpr float kSlack = 8.f;
 template <int D>
 struct FwdCfg {
   static constexpr int BN = D == 128 ? 64 : 128;
+  using Line = BiasLine<127 + BN, false>;
   static constexpr int kTile = BN * D * 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 128 * D * 2;
   static constexpr int OFF_V = OFF_K + 2 * kTile;
   static constexpr int OFF_BIAS = OFF_V + 2 * kTile;
-  static constexpr int OFF_BAR = OFF_BIAS + 2 * ((int)sizeof(BiasLine<BN>) + 15) / 16 * 16;
+  static constexpr int OFF_BAR = OFF_BIAS + (2 * (int)sizeof(Line) + 15) / 16 * 16;
   static constexpr int SMEM = OFF_BAR + 256;
   static constexpr int kColP = BN, kColO = BN + BN / 2;
   static constexpr uint32_t kTmem = 256;
@@ -66,8 +67,9 @@ template <class T, int D>
 __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_constant__ BiasAttnArgs a, Split sp) {
   using C = FwdCfg<D>;
   constexpr int BN = C::BN;
+  using Line = typename C::Line;
   extern __shared__ __align__(1024) uint8_t smem[];
-  BiasLine<BN>* lines = reinterpret_cast<BiasLine<BN>*>(smem + C::OFF_BIAS);
+  Line* lines = reinterpret_cast<Line*>(smem + C::OFF_BIAS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* k_full = bars;         // [2]
   uint64_t* k_free = bars + 2;     // [2]
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
       load_tile<T, D, BN, kProducers>(sk + s * C::kTile, kh, a.k.st, j0, nk, p);
       cp_async_mbar_arrive_noinc(&k_full[s]);
       if (t >= 2 && !warp_wait(&b_free[s], parity, a.ctx, kErrAttnLoad)) break;
-      fill_bias_line<T, BN, kProducers>(&lines[s], a, h, j0 - pos0, p);
+      fill_bias_line<T, 127 + BN, false, kProducers>(&lines[s], a, h, j0 - pos0 - 127, p);
       mbar_arrive(&b_full[s]);
       if (t >= 2 && !warp_wait(&v_free[s], parity, a.ctx, kErrAttnLoad)) break;
       load_tile<T, D, BN, kProducers>(sv + s * C::kTile, vh, a.v.st, j0, nk, p);
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
            warp_wait(s_full, t & 1, a.ctx, kErrAttnSoftmax);
       if (!ok) break;
       tc_fence_after();
-      const BiasLine<BN>& bl = lines[s];
+      const Line& bl = lines[s];
       const bool flat = bl.same[0] && bl.same[1];
       const float value = bl.value;
       const float* line = bl.line + 127 - (warp * 32 + lane);

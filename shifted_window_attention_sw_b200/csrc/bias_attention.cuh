@@ -62,14 +62,6 @@ __device__ __forceinline__ float bias_of(const BiasAttnArgs& a, int rel, int h, 
   return v <= kExclude ? -INFINITY : v;
 }
 
-// The same in units of log2, with the causal rule (a key behind the query's
-// position is taken out) folded in.
-template <class T>
-__device__ __forceinline__ float bias2_of(const BiasAttnArgs& a, int rel, int h) {
-  const float v = bias_of<T>(a, rel, h) * kLog2E;
-  return a.causal && rel > 0 ? -INFINITY : v;
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -153,35 +145,51 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx.err, code, ctx.wait_limit));
 }
 
-// The bias of a 128 x BN tile as one line: entry t holds the offset base + t -
-// 127, so that row i and column j read entry j - i + 127. Written by `THREADS`
-// threads; `same` of each of their warps says whether all its entries equal
-// `value` (far tiles have one bucket: their rows read no line at all).
-template <int BN>
+// The bias of a 128 x BN tile depends on the offset of key and query alone, so
+// it is one line of N = 127 + BN values, entry t at offset base + t: row i and
+// column j read entry j - i + 127 (rows are queries) or i - j + BN - 1 (rows are
+// keys). Written by whole warps; `same` of each warp says whether all its
+// entries equal entry 0, `value` and `which` (far tiles have one bucket: their
+// rows read no line at all). With kBuckets the buckets are kept too, and
+// entries are the same only if their buckets are.
+template <int N, bool kBuckets>
 struct BiasLine {
-  float line[128 + BN];
+  float line[N + 1];
+  uint16_t bucket[kBuckets ? N + 1 : 2];
   float value;
-  int same[4];
+  int which;
+  int same[2];
 };
-template <class T, int BN, int THREADS>
-__device__ __forceinline__ void fill_bias_line(BiasLine<BN>* o, const BiasAttnArgs& a, int h, int base, int p) {
-  const float first = bias2_of<T>(a, base, h);
+template <class T, int N, bool kBuckets, int THREADS>
+__device__ __forceinline__ void fill_bias_line(BiasLine<N, kBuckets>* o, const BiasAttnArgs& a, int h, int base, int p) {
+  static_assert(THREADS == 64, "two warps");
+  int which = 0;
+  auto entry = [&](int rel, int* k) {
+    const float v = bias_of<T>(a, rel, h, k) * kLog2E;
+    return a.causal && rel > 0 ? -INFINITY : v;  // the causal rule is part of the line
+  };
+  const float first = entry(base, &which);
   bool same = true;
-  // a tile beyond the map's ends, on one side of the causal border
-  const bool far = base - 127 >= a.D + 1 || base + BN - 1 <= -a.D;
+  // a tile beyond one of the map's ends, on one side of the causal border
+  const bool far = base > a.D || base + N - 1 <= -a.D;
   if (!far) {
 #pragma unroll
-    for (int t = 0; t < 127 + BN; t += THREADS) {
-      if (t + p < 127 + BN) {
-        const float v = bias2_of<T>(a, base + t + p - 127, h);
+    for (int t = 0; t < N; t += THREADS) {
+      if (t + p < N) {
+        int k = 0;
+        const float v = entry(base + t + p, &k);
         o->line[t + p] = v;
-        same = same && v == first;
+        if (kBuckets) o->bucket[t + p] = (uint16_t)k;
+        same = same && v == first && (!kBuckets || k == which);
       }
     }
   }
   same = __all_sync(0xffffffffu, same);
   if ((p & 31) == 0) o->same[p >> 5] = same;
-  if (p == 0) o->value = first;
+  if (p == 0) {
+    o->value = first;
+    o->which = which;
+  }
 }
 
 }  // namespace vswin

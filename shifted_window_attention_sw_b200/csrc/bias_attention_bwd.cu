@@ -1,135 +1,490 @@
-// Gradient of the attention with bucketed bias.
+// Gradient of the attention with bucketed bias. With the forward's P (rebuilt
+// from lse), dP = dO v^T and D_i = dO_i . o_i:
+//
+//   dS = P (dP - D),  dq = scale dS k,  dk = scale dS^T q,  dv = P^T dO,
+//   dtable[bucket][h] = sum of dS over the pairs of that bucket.
+//
+// Two passes of one kernel, each with 128 fixed rows and moving tiles of 64
+// rows: queries fixed (dq and the table's gradient; it also leaves D for the
+// other pass), then keys fixed (dk and dv, summed over the heads that share
+// them). Each recomputes S and dP on tcgen05 (7 products instead of the 5 of a
+// single pass), and in return every sum has one owner and a fixed order: no
+// atomics, the same result for the same call.
+//
+// Per tile: X = F1 M1^T and Y = F2 M2^T into TMEM (fp32; queries fixed: F = q,
+// dO and M = k, v; keys fixed: F = k, v and M = q, dO), four warps (TMEM lane =
+// fixed row) form P and dS and write them back as 16-bit operands over the
+// scores, then the sums += dS M1 (and P M2) as TS MMAs. D = 32 and 64: one such
+// group of warps, two CTAs per SM; D = 128: two groups on alternating tiles with
+// a score buffer each, one CTA per SM (the sums take 256 TMEM columns).
+//
+// The table's gradient sums dS along diagonals (the bias is one line per tile,
+// see BiasLine). A tile of one bucket adds its rows' sums. In the others a
+// warp passes partial sums from lane to lane: after column c, lane 31 holds the
+// finished sum of diagonal c - 31; the 95 diagonals of its 32 rows then go to
+// the warp's bins, equal buckets combined in lane order.
 #include "bias_attention.cuh"
 
 namespace vswin {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kBn = 64;             // moving rows per tile
+constexpr int kLineN = 127 + kBn;   // offsets in a tile
+constexpr int kProducers = 64;
 
-// One query row per warp: D = dO . o, dS = P (dP - D), dq = scale dS k.
-template <class T>
-__global__ void __launch_bounds__(32 * kWarps) attn_dq_kernel(BiasAttnArgs a, float* D, float* dtab) {
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.hq * a.Lq) return;
-  const int i = (int)(row % a.Lq), h = (int)(row / a.Lq % a.hq), b = (int)(row / a.Lq / a.hq);
-  const int hk = h / (a.hq / a.hk);
+template <int D, bool kKeys>
+struct BwdCfg {
+  static constexpr int G = D == 128 ? 2 : 1;  // groups of four warps
+  static constexpr int CTAS = D == 128 ? 1 : 2;
+  static constexpr int ST = 3;  // stages of the moving tiles
+  static constexpr int THREADS = 32 * (4 * G + 3);
+  using Line = BiasLine<kLineN, !kKeys>;
+  static constexpr int kFixed = 128 * D * 2, kMoving = kBn * D * 2;
+  static constexpr int OFF_F = 0;                                   // F1, F2
+  static constexpr int OFF_M = 2 * kFixed;                          // per stage M1, M2
+  static constexpr int OFF_LINE = OFF_M + ST * 2 * kMoving;
+  static constexpr int OFF_COL = OFF_LINE + (ST * (int)sizeof(Line) + 15) / 16 * 16;  // per stage and column (-lse, -D)
+  static constexpr int OFF_DIAG = OFF_COL + (kKeys ? ST * kBn * 8 : 0);
+  static constexpr int OFF_BAR = OFF_DIAG + (kKeys ? 0 : 4 * G * 96 * 4);
+  static constexpr int OFF_BINS = OFF_BAR + 192;                    // [4 G][buckets], queries fixed
+  static constexpr uint32_t kTmem = D == 128 ? 512 : 256;
+  static constexpr int kColAcc = 128 * G;  // sums behind the score buffers
+  static_assert(kColAcc + (kKeys ? 2 : 1) * D <= (int)kTmem, "TMEM columns of a CTA");
+};
+
+struct BwdArgs {
+  BiasAttnArgs a;
+  float* delta;    // [B][hq][Lq] D
+  float* dtab;     // [hq][B * query tiles][buckets] shares of the table's gradient
+};
+
+template <class T, int D, bool kKeys>
+__global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::CTAS)
+    attn_bwd_kernel(const __grid_constant__ BwdArgs args) {
+  using C = BwdCfg<D, kKeys>;
+  using Line = typename C::Line;
+  constexpr int G = C::G, ST = C::ST;
+  constexpr int kMmaWarp = 4 * G;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const BiasAttnArgs& a = args.a;
+  Line* lines = reinterpret_cast<Line*>(smem + C::OFF_LINE);
+  float2* cols = reinterpret_cast<float2*>(smem + C::OFF_COL);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* full = bars;            // [ST] moving tiles, line and columns
+  uint64_t* free_ = bars + ST;      // [ST] their MMAs and reads are done
+  uint64_t* s_full = bars + 2 * ST;       // [G] scores in TMEM
+  uint64_t* ds_full = s_full + G;         // [G] operands written back
+  uint64_t* f_full = ds_full + G;         // fixed tiles
+  uint64_t* done = f_full + 1;            // every sum accumulated
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ft = (int)((gridDim.x - 1 - blockIdx.x) / (a.B * (kKeys ? a.hk : a.hq)));
+  const int rest = (int)((gridDim.x - 1 - blockIdx.x) % (a.B * (kKeys ? a.hk : a.hq)));
+  const int fixed_tiles = gridDim.x / (a.B * (kKeys ? a.hk : a.hq));
+  const int group = a.hq / a.hk;
+  const int hf = rest % (kKeys ? a.hk : a.hq), b = rest / (kKeys ? a.hk : a.hq);
+  const int hk = kKeys ? hf : hf / group;
   const SeqLens sl = seq_lens(a, b);
-  const int pos = sl.start + i;
-  const T* q = static_cast<const T*>(a.q.p) + a.q.at(b, i, h);
-  const T* o = static_cast<const T*>(a.o.p) + a.o.at(b, i, h);
-  const T* go = static_cast<const T*>(a.dout.p) + a.dout.at(b, i, h);
-  const float lse = a.lse[row];
-  const int nk = i < sl.nq && lse > -INFINITY ? (a.causal ? min(sl.nk, pos + 1) : sl.nk) : 0;
-  float dd = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  if (nk > 0)
-    for (int c = lane; c < a.d; c += 32) dd = fmaf(to_f(o[c]), to_f(go[c]), dd);
-  for (int k = 16; k; k >>= 1) dd += __shfl_xor_sync(~0u, dd, k);
-  if (lane == 0) D[row] = dd;
-  for (int j0 = 0; j0 < nk; j0 += 32) {
-    const int j = j0 + lane;
-    float ds = 0.f;
-    if (j < nk) {
-      const T* k = static_cast<const T*>(a.k.p) + a.k.at(b, j, hk);
-      const T* v = static_cast<const T*>(a.v.p) + a.v.at(b, j, hk);
-      float s = 0.f, dp = 0.f;
-      for (int c = 0; c < a.d; ++c) {
-        s = fmaf(to_f(q[c]), to_f(k[c]), s);
-        dp = fmaf(to_f(go[c]), to_f(v[c]), dp);
-      }
-      int bucket;
-      s = s * a.scale + bias_of<T>(a, j - pos, h, &bucket);
-      ds = expf(s - lse) * (dp - dd);
-      if (ds != 0.f) atomicAdd(&dtab[(long long)bucket * a.hq + h], ds);
-    }
-    for (int jj = 0; jj < 32 && j0 + jj < nk; ++jj) {
-      const float x = __shfl_sync(~0u, ds, jj);
-      const T* k = static_cast<const T*>(a.k.p) + a.k.at(b, j0 + jj, hk);
-      for (int c = 0; c < a.d / 32; ++c) acc[c] = fmaf(x, to_f(k[lane + 32 * c]), acc[c]);
-    }
+  // causal: the heavy fixed tiles are the last queries and the first keys
+  const int f0 = (kKeys ? fixed_tiles - 1 - ft : ft) * 128;
+  // moving rows [m_lo, m_hi) that some fixed row meets
+  int m_lo = 0, m_hi;
+  if (kKeys) {
+    m_hi = f0 < sl.nk ? sl.nq : 0;
+    if (a.causal) m_lo = min(max(0, f0 - sl.start), m_hi) / kBn * kBn;
+  } else {
+    m_hi = f0 < sl.nq ? sl.nk : 0;
+    if (a.causal) m_hi = min(m_hi, max(0, sl.start + min(f0 + 128, sl.nq)));
   }
-  T* dq = static_cast<T*>(a.dq.p) + a.dq.at(b, i, h);
-  for (int c = 0; c < a.d / 32; ++c) dq[lane + 32 * c] = from_f<T>(acc[c] * a.scale);
-}
+  const int per_head = (m_hi - m_lo + kBn - 1) / kBn;
+  const int nt = per_head * (kKeys ? group : 1);
 
-// One key row per warp: dv = P^T dO and dk = scale dS^T q over the queries and heads that read it.
-template <class T>
-__global__ void __launch_bounds__(32 * kWarps) attn_dkv_kernel(BiasAttnArgs a, const float* D) {
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.hk * a.Lk) return;
-  const int j = (int)(row % a.Lk), hk = (int)(row / a.Lk % a.hk), b = (int)(row / a.Lk / a.hk);
-  const SeqLens sl = seq_lens(a, b);
-  const T* k = static_cast<const T*>(a.k.p) + a.k.at(b, j, hk);
-  const T* v = static_cast<const T*>(a.v.p) + a.v.at(b, j, hk);
-  float dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-  const int i_lo = a.causal ? max(0, j - sl.start) : 0;
-  const int i_hi = j < sl.nk ? sl.nq : 0;
-  for (int h = hk * (a.hq / a.hk); h < (hk + 1) * (a.hq / a.hk); ++h)
-    for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
-      const int i = i0 + lane;
-      float p = 0.f, ds = 0.f;
-      if (i < i_hi) {
-        const long long r = ((long long)b * a.hq + h) * a.Lq + i;
-        const float lse = a.lse[r];
-        if (lse > -INFINITY) {
-          const T* q = static_cast<const T*>(a.q.p) + a.q.at(b, i, h);
-          const T* go = static_cast<const T*>(a.dout.p) + a.dout.at(b, i, h);
-          float s = 0.f, dp = 0.f;
-          for (int c = 0; c < a.d; ++c) {
-            s = fmaf(to_f(q[c]), to_f(k[c]), s);
-            dp = fmaf(to_f(go[c]), to_f(v[c]), dp);
+  if (tid == 0) {
+    for (int k = 0; k < ST; ++k) {
+      mbar_init(&full[k], 2 * kProducers);
+      mbar_init(&free_[k], 1 + 4);
+    }
+    for (int k = 0; k < G; ++k) {
+      mbar_init(&s_full[k], 1);
+      mbar_init(&ds_full[k], 4);
+    }
+    mbar_init(f_full, kProducers);
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(s_tmem, C::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t sf = smem_u32(smem + C::OFF_F), sm = smem_u32(smem + C::OFF_M);
+
+  if (warp > kMmaWarp) {
+    // ------------------------------------------------------------ producers
+    const int p = tid - 32 * (kMmaWarp + 1);
+    const Heads &F1 = kKeys ? a.k : a.q, &F2 = kKeys ? a.v : a.dout, &M1 = kKeys ? a.q : a.k, &M2 = kKeys ? a.dout : a.v;
+    const int fn = kKeys ? sl.nk : sl.nq;
+    if (nt > 0) {
+      load_tile<T, D, 128, kProducers>(sf, static_cast<const T*>(F1.p) + F1.at(b, 0, hf), F1.st, f0, fn, p);
+      load_tile<T, D, 128, kProducers>(sf + C::kFixed, static_cast<const T*>(F2.p) + F2.at(b, 0, hf), F2.st, f0, fn, p);
+      cp_async_mbar_arrive_noinc(f_full);
+    }
+    int s = 0, u = 0, r0 = m_lo, h = kKeys ? hk * group : hf;
+    uint32_t parity = 1;  // of the stage's previous use
+    for (int t = 0; t < nt; ++t) {
+      if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad)) break;
+      const int hm = kKeys ? h : hk;
+      const uint32_t dst = sm + s * 2 * C::kMoving;
+      load_tile<T, D, kBn, kProducers>(dst, static_cast<const T*>(M1.p) + M1.at(b, 0, hm), M1.st, r0, m_hi, p);
+      load_tile<T, D, kBn, kProducers>(dst + C::kMoving, static_cast<const T*>(M2.p) + M2.at(b, 0, hm), M2.st, r0, m_hi, p);
+      cp_async_mbar_arrive_noinc(&full[s]);
+      if constexpr (kKeys) {
+        float2 c = make_float2(-INFINITY, 0.f);  // a query that takes no part: P = 0
+        if (r0 + p < m_hi) {
+          const long long r = ((long long)b * a.hq + h) * a.Lq + r0 + p;
+          const float lse = a.lse[r];
+          if (lse != -INFINITY) c = make_float2(-lse * kLog2E, -args.delta[r]);
+        }
+        cols[s * kBn + p] = c;
+        fill_bias_line<T, kLineN, false, kProducers>(&lines[s], a, h, f0 - (sl.start + r0) - (kBn - 1), p);
+      } else {
+        fill_bias_line<T, kLineN, true, kProducers>(&lines[s], a, h, r0 - (sl.start + f0) - 127, p);
+      }
+      mbar_arrive(&full[s]);
+      if (++s == ST) s = 0, parity ^= 1;
+      r0 += kBn;
+      if (++u == per_head) u = 0, r0 = m_lo, ++h;
+    }
+    cp_async_wait_all();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0 && nt > 0) {
+      constexpr uint32_t id_s = idesc16<T>(128, kBn, 0, 0), id_acc = idesc16<T>(128, D, 0, 1);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return mbar_wait(bar, parity, a.ctx.err, kErrAttnMma, a.ctx.wait_limit);
+      };
+      int ss = 0;        // stage and parity of the next scores' tile
+      uint32_t sp = 0;
+      auto scores = [&](int t) {
+        if (!wait(&full[ss], sp)) return false;
+        fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
+        tc_fence_after();
+        const uint32_t buf = tmem + 128 * (t % G), m1 = sm + ss * 2 * C::kMoving;
+        mma_rows<D>(buf, sf, m1, id_s);
+        mma_rows<D>(buf + 64, sf + C::kFixed, m1 + C::kMoving, id_s);
+        umma_commit(&s_full[t % G]);
+        if (++ss == ST) ss = 0, sp ^= 1;
+        return true;
+      };
+      bool ok = wait(f_full, 0);
+      fence_proxy_async_smem();
+      for (int t = 0; t < G && t < nt && ok; ++t) ok = scores(t);
+      int as = 0;
+      for (int t = 0; t < nt && ok; ++t) {
+        ok = wait(&ds_full[t % G], (t / G) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t buf = tmem + 128 * (t % G), m1 = sm + as * 2 * C::kMoving;
+        if (kKeys) {
+          mma_acc<D, kBn>(tmem + C::kColAcc, buf + 64, m1, id_acc, t == 0);                   // dk += dS^T q
+          mma_acc<D, kBn>(tmem + C::kColAcc + D, buf, m1 + C::kMoving, id_acc, t == 0);       // dv += P^T dO
+        } else {
+          mma_acc<D, kBn>(tmem + C::kColAcc, buf + 64, m1, id_acc, t == 0);                   // dq += dS k
+        }
+        umma_commit(&free_[as]);
+        if (t == nt - 1) umma_commit(done);
+        if (++as == ST) as = 0;
+        if (t + G < nt) ok = scores(t + G);  // runs after the sums, which read these columns
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ P and dS
+    const int g = warp >> 2;
+    const int row = (warp & 3) * 32 + lane, i = f0 + row;
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t buf = tmem + tl + 128 * g;
+    const float c = a.scale * kLog2E;
+    const float2 c2 = make_float2(c, c);
+    float* bins = reinterpret_cast<float*>(smem + C::OFF_BINS) + warp * a.buckets;
+    float* diag = reinterpret_cast<float*>(smem + C::OFF_DIAG) + warp * 96;
+    float nl = -INFINITY, nd = 0.f;  // queries fixed: -lse (log2) and -D of the row
+    float flat_sum = 0.f;            // dS of tiles of one bucket, until the bucket changes
+    int flat_bucket = 0;
+    if (!kKeys) {
+      for (int k = lane; k < a.buckets; k += 32) bins[k] = 0.f;
+      if (i < a.Lq) {
+        const long long r = ((long long)b * a.hq + hf) * a.Lq + i;
+        float dd = 0.f;
+        if (i < sl.nq) {
+          const float lse = a.lse[r];
+          if (lse != -INFINITY) {
+            const T* o = static_cast<const T*>(a.o.p) + a.o.at(b, i, hf);
+            const T* go = static_cast<const T*>(a.dout.p) + a.dout.at(b, i, hf);
+#pragma unroll
+            for (int k = 0; k < D; k += 8) {
+              const uint4 ou = *reinterpret_cast<const uint4*>(o + k), gu = *reinterpret_cast<const uint4*>(go + k);
+              const T *oe = reinterpret_cast<const T*>(&ou), *ge = reinterpret_cast<const T*>(&gu);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dd = fmaf(to_f(oe[e]), to_f(ge[e]), dd);
+            }
+            nl = -lse * kLog2E;
+            nd = -dd;
           }
-          p = expf(s * a.scale + bias_of<T>(a, j - sl.start - i, h) - lse);
-          ds = p * (dp - D[r]);
+        }
+        if (g == 0) args.delta[r] = dd;
+      }
+      __syncwarp();
+    }
+    // a bucket's sum over the warp goes to its bin
+    auto flush_flat = [&]() {
+      float v = flat_sum;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) bins[flat_bucket] += v;
+      __syncwarp();
+      flat_sum = 0.f;
+    };
+    int s = g;
+    uint32_t sp = 0;
+    bool ok = true;
+    for (int t = g; t < nt; t += G) {
+      ok = warp_wait(&full[s], sp, a.ctx, kErrAttnSoftmax) && warp_wait(&s_full[g], (t / G) & 1, a.ctx, kErrAttnSoftmax);
+      if (!ok) break;
+      tc_fence_after();
+      const Line& bl = lines[s];
+      const bool flat = bl.same[0] && bl.same[1];
+      const float value = bl.value;
+      const float* line = bl.line + (kKeys ? kBn - 1 + row : 127 - row);
+      const float2* col = cols + s * kBn;
+      const int live = kKeys ? kBn : m_hi - t * kBn;  // queries fixed: columns of the tile that are keys
+      float2 sum = make_float2(0.f, 0.f);
+      float acc = 0.f;
+      if (!kKeys && flat && bl.which != flat_bucket) {
+        flush_flat();
+        flat_bucket = bl.which;
+      }
+#pragma unroll
+      for (int c0 = 0; c0 < kBn; c0 += 32) {
+        uint32_t us[32], ud[32], w[16];
+        tmem_ld32(buf + c0, us);
+        tmem_ld32(buf + 64 + c0, ud);
+        tmem_wait_ld_keep(us);
+        tmem_wait_ld_keep(ud);
+        float ds[32];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float2 off, d2;
+          if (kKeys) {
+            const float4 q = *reinterpret_cast<const float4*>(col + c0 + k);  // two columns' (-lse, -D)
+            off = make_float2(q.x, q.z);
+            d2 = make_float2(q.y, q.w);
+          } else {
+            off = make_float2(nl, nl);
+            d2 = make_float2(nd, nd);
+          }
+          if (flat)
+            off = __fadd2_rn(off, make_float2(value, value));
+          else if (kKeys)
+            off = __fadd2_rn(off, make_float2(line[-(c0 + k)], line[-(c0 + k + 1)]));
+          else
+            off = __fadd2_rn(off, make_float2(line[c0 + k], line[c0 + k + 1]));
+          float2 x = __ffma2_rn(make_float2(__uint_as_float(us[k]), __uint_as_float(us[k + 1])), c2, off);
+          if (!kKeys && live < kBn) {
+            x.x = c0 + k < live ? x.x : -INFINITY;
+            x.y = c0 + k + 1 < live ? x.y : -INFINITY;
+          }
+          const float2 pr = make_float2(ex2(x.x), ex2(x.y));
+          const float2 e =
+              __fmul2_rn(pr, __fadd2_rn(make_float2(__uint_as_float(ud[k]), __uint_as_float(ud[k + 1])), d2));
+          if (kKeys) us[k / 2] = pack2<T>(pr.x, pr.y);
+          w[k / 2] = pack2<T>(e.x, e.y);
+          ds[k] = e.x;
+          ds[k + 1] = e.y;
+          if (!kKeys && flat) sum = __fadd2_rn(sum, e);
+        }
+        if (kKeys) tmem_st16(buf + c0 / 2, us);
+        tmem_st16(buf + 64 + c0 / 2, w);
+        if (!kKeys && !flat) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float up = __shfl_up_sync(0xffffffffu, acc, 1);
+            acc = (lane == 0 ? 0.f : up) + ds[k];
+            if (lane == 31) diag[c0 + k] = acc;
+          }
         }
       }
-      for (int ii = 0; ii < 32 && i0 + ii < i_hi; ++ii) {
-        const float x = __shfl_sync(~0u, p, ii), y = __shfl_sync(~0u, ds, ii);
-        const T* q = static_cast<const T*>(a.q.p) + a.q.at(b, i0 + ii, h);
-        const T* go = static_cast<const T*>(a.dout.p) + a.dout.at(b, i0 + ii, h);
-        for (int c = 0; c < a.d / 32; ++c) {
-          dv[c] = fmaf(x, to_f(go[lane + 32 * c]), dv[c]);
-          dk[c] = fmaf(y, to_f(q[lane + 32 * c]), dk[c]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[g]);
+      if (!kKeys) {
+        if (flat) {
+          flat_sum += sum.x + sum.y;
+        } else {
+          if (lane < 31) diag[kBn - 1 + 31 - lane] = acc;
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const int at = lane + 32 * k;  // diagonal at - 31
+            const bool have = at < kBn + 31;
+            float v = have ? diag[at] : 0.f;
+            const int bucket = have ? bl.bucket[at + 96 - 32 * (warp & 3)] : -1;
+            // a run of one bucket adds up into its last lane
+            const int before = __shfl_up_sync(0xffffffffu, bucket, 1);
+            const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 || before != bucket);
+            const int start = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+              const float x = __shfl_up_sync(0xffffffffu, v, o);
+              if (lane - o >= start) v += x;
+            }
+            const bool tail = lane == 31 || ((heads >> (lane + 1)) & 1);
+            // runs that share a bucket (no map of vswin_bucket_map has them) add up into the first
+            const uint32_t equal = __match_any_sync(0xffffffffu, tail && have ? bucket : -2 - lane);
+            const bool first = (equal & ((1u << lane) - 1)) == 0;
+            uint32_t others = first ? equal & ~(1u << lane) : 0;
+            while (__any_sync(0xffffffffu, others != 0)) {
+              const float x = __shfl_sync(0xffffffffu, v, others ? __ffs(others) - 1 : lane);
+              if (others) {
+                v += x;
+                others &= others - 1;
+              }
+            }
+            if (tail && have && first) bins[bucket] += v;
+            __syncwarp();
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&free_[s]);
+      s += G;
+      if (s >= ST) s -= ST, sp ^= 1;
+    }
+    if (!kKeys) flush_flat();
+    if (ok && nt > 0) ok = warp_wait(done, 0, a.ctx, kErrAttnSoftmax);
+    tc_fence_after();
+    if (ok) {
+      // queries fixed: group g writes its part of dq's channels; keys fixed: dk and dv, one group each when there are two
+      const int n_out = kKeys ? a.Lk : a.Lq;
+      const bool some = i < (kKeys ? sl.nk : sl.nq) && nt > 0;
+      constexpr int kOuts = kKeys && G == 1 ? 2 : 1;
+      constexpr int kCols = !kKeys && G == 2 ? D / 2 : D;
+#pragma unroll
+      for (int o = 0; o < kOuts; ++o) {
+        const int which = kOuts == 2 ? o : g;  // keys fixed: 0 dk, 1 dv
+        const Heads& out = !kKeys ? a.dq : (which == 0 ? a.dk : a.dv);
+        const float scale = kKeys && which == 1 ? 1.f : a.scale;
+        const int first = !kKeys && G == 2 ? g * kCols : 0;
+        const uint32_t from = tmem + tl + C::kColAcc + (kKeys ? which * D : 0) + first;
+        T* dst = static_cast<T*>(out.p) + (i < n_out ? out.at(b, i, hf) : 0) + first;
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 16) {
+          uint32_t u[16];
+          if (nt > 0) {
+            tmem_ld16(from + c0, u);
+            tmem_wait_ld_keep(u);
+          }
+          float f[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) f[k] = some ? __uint_as_float(u[k]) * scale : 0.f;
+          if (i < n_out) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 8)
+              *reinterpret_cast<uint4*>(dst + c0 + k) =
+                  make_uint4(pack2<T>(f[k], f[k + 1]), pack2<T>(f[k + 2], f[k + 3]), pack2<T>(f[k + 4], f[k + 5]),
+                             pack2<T>(f[k + 6], f[k + 7]));
+          }
         }
       }
     }
-  T* ok = static_cast<T*>(a.dk.p) + a.dk.at(b, j, hk);
-  T* ov = static_cast<T*>(a.dv.p) + a.dv.at(b, j, hk);
-  for (int c = 0; c < a.d / 32; ++c) {
-    ok[lane + 32 * c] = from_f<T>(dk[c] * a.scale);
-    ov[lane + 32 * c] = from_f<T>(dv[c]);
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+  if (!kKeys) {  // this CTA's share of the table's gradient
+    const float* bins = reinterpret_cast<const float*>(smem + C::OFF_BINS);
+    float* out = args.dtab + (((long long)hf * a.B + b) * fixed_tiles + f0 / 128) * a.buckets;
+    for (int k = tid; k < a.buckets; k += C::THREADS) {
+      float v = 0.f;
+      for (int w = 0; w < 4 * G; ++w) v += bins[w * a.buckets + k];
+      out[k] = v;
+    }
   }
 }
 
+// dtable = the CTAs' shares of a head added in a fixed order: 32 buckets per
+// block, eight runs of shares side by side.
 template <class T>
-__global__ void dtable_round_kernel(BiasAttnArgs a, const float* dtab) {
-  const int n = a.buckets * a.hq;
-  for (int k = blockIdx.x * blockDim.x + threadIdx.x; k < n; k += gridDim.x * blockDim.x)
-    static_cast<T*>(a.dtable)[k] = from_f<T>(dtab[k]);
+__global__ void __launch_bounds__(256) attn_dtable_kernel(const float* dtab, int shares, int buckets, int hq, T* out) {
+  __shared__ float s[8][33];
+  const int h = blockIdx.x, lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int k = blockIdx.y * 32 + lane;
+  float v = 0.f;
+  if (k < buckets)
+    for (int c = run; c < shares; c += 8) v += dtab[((long long)h * shares + c) * buckets + k];
+  s[run][lane] = v;
+  __syncthreads();
+  if (run == 0 && k < buckets) {
+    for (int r = 1; r < 8; ++r) v += s[r][lane];
+    out[(long long)k * hq + h] = from_f<T>(v);
+  }
+}
+
+template <class T, int D, bool kKeys>
+cudaError_t pass(const BwdArgs& args, cudaStream_t st) {
+  using C = BwdCfg<D, kKeys>;
+  const BiasAttnArgs& a = args.a;
+  const int smem = C::OFF_BINS + (kKeys ? 0 : 4 * C::G * a.buckets * 4);
+  constexpr int kMost = C::OFF_BINS + (kKeys ? 0 : 4 * C::G * kMaxBuckets * 4);
+  static_assert(C::CTAS * (kMost + 1024) <= 228 * 1024, "shared memory of an SM");
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<T, D, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (e != cudaSuccess) return e;
+  const long long grid = (long long)a.B * (kKeys ? a.hk : a.hq) * (((kKeys ? a.Lk : a.Lq) + 127) / 128);
+  prof_begin(kKindAttnBwd, st);
+  attn_bwd_kernel<T, D, kKeys><<<(unsigned)grid, C::THREADS, smem, st>>>(args);
+  prof_end(kKindAttnBwd, st);
+  count_launch();
+  return cudaGetLastError();
+}
+
+size_t delta_bytes(const BiasAttnArgs& a) { return ((size_t)a.B * a.hq * a.Lq * 4 + 255) / 256 * 256; }
+
+template <class T, int D>
+cudaError_t backward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
+  BwdArgs args{a, static_cast<float*>(scratch), reinterpret_cast<float*>(static_cast<char*>(scratch) + delta_bytes(a))};
+  cudaError_t e = pass<T, D, false>(args, st);
+  if (e == cudaSuccess) e = pass<T, D, true>(args, st);
+  if (e != cudaSuccess) return e;
+  prof_begin(kKindOther, st);
+  attn_dtable_kernel<T><<<dim3(a.hq, (a.buckets + 31) / 32), 256, 0, st>>>(args.dtab, a.B * ((a.Lq + 127) / 128), a.buckets,
+                                                                          a.hq, static_cast<T*>(a.dtable));
+  prof_end(kKindOther, st);
+  count_launch();
+  return cudaGetLastError();
 }
 
 template <class T>
-cudaError_t backward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
-  const long long rows = (long long)a.B * a.hq * a.Lq, keys = (long long)a.B * a.hk * a.Lk;
-  float* D = static_cast<float*>(scratch);
-  float* dtab = D + rows;
-  cudaError_t e = cudaMemsetAsync(dtab, 0, (size_t)a.buckets * a.hq * 4, st);
-  if (e != cudaSuccess) return e;
-  attn_dq_kernel<T><<<(unsigned)((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(a, D, dtab);
-  attn_dkv_kernel<T><<<(unsigned)((keys + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(a, D);
-  dtable_round_kernel<T><<<(a.buckets * a.hq + 255) / 256, 256, 0, st>>>(a, dtab);
-  count_launch(3);
-  return cudaGetLastError();
+cudaError_t backward_d(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
+  if (a.d == 32) return backward<T, 32>(a, scratch, st);
+  if (a.d == 64) return backward<T, 64>(a, scratch, st);
+  return backward<T, 128>(a, scratch, st);
 }
 
 }  // namespace
 
 size_t bias_attention_backward_scratch_bytes(const BiasAttnArgs& a) {
-  return ((size_t)a.B * a.hq * a.Lq + (size_t)a.buckets * a.hq) * 4;
+  return delta_bytes(a) + (size_t)a.hq * a.B * ((a.Lq + 127) / 128) * a.buckets * 4;
 }
 cudaError_t launch_bias_attention_backward(const BiasAttnArgs& a, int dtype, void* scratch, cudaStream_t st) {
-  return dtype == kBF16 ? backward<__nv_bfloat16>(a, scratch, st) : backward<__half>(a, scratch, st);
+  return dtype == kBF16 ? backward_d<__nv_bfloat16>(a, scratch, st) : backward_d<__half>(a, scratch, st);
 }
 
 }  // namespace vswin

@@ -164,8 +164,8 @@ int check_bias_attention(int dtype, int B, int Lq, int Lk, int hq, int hk, int d
   if (!bias || !bias->table || !bias->map) return fail(VSWIN_ERR_INVALID_ARG, "bias, its table or its map is NULL");
   if (!aligned(bias->table, 2) || !aligned(bias->map, 4))
     return fail(VSWIN_ERR_INVALID_ARG, "bias table or map is misaligned");
-  if (bias->buckets <= 0 || bias->buckets > 4096 || bias->max_distance < 0 || bias->max_distance > (1 << 20))
-    return fail(VSWIN_ERR_INVALID_ARG, "buckets %d must lie in [1, 4096] and max_distance %d in [0, 2^20]",
+  if (bias->buckets <= 0 || bias->buckets > kMaxBuckets || bias->max_distance < 0 || bias->max_distance > (1 << 20))
+    return fail(VSWIN_ERR_INVALID_ARG, "buckets %d must lie in [1, 1024] and max_distance %d in [0, 2^20]",
                 bias->buckets, bias->max_distance);
   a->table = bias->table, a->map = bias->map, a->buckets = bias->buckets, a->D = bias->max_distance;
   if (vis) {
