@@ -31,6 +31,7 @@
 // Bound: one exponential per visible pair (16 per clock and SM) for D = 32 and
 // 64, the tensor cores for D = 128.
 #include "bias_attention.cuh"
+#include "bias_attention_split.h"
 
 namespace vswin {
 namespace {
@@ -55,12 +56,6 @@ struct FwdCfg {
   static constexpr int kColP = BN, kColO = BN + BN / 2;
   static constexpr uint32_t kTmem = 256;
   static_assert(kColO + D <= 256, "TMEM columns of a CTA");
-};
-
-struct Split {
-  int n;            // splits of the keys (1: results go out directly)
-  float* o;         // [n][B hq Lq][D]
-  float* lse;       // [n][B hq Lq], log2
 };
 
 template <class T, int D>
@@ -329,32 +324,48 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
   }
 }
 
+// Parts of the keys when the query tiles alone leave SMs idle: as many as fill
+// two CTAs per SM, at least four key tiles in each.
+int forward_splits(const BiasAttnArgs& a) {
+  const int bn = a.d == 128 ? 64 : 128;
+  const long long ctas = (long long)a.B * a.hq * ((a.Lq + 127) / 128), slots = 2LL * sm_count();
+  const long long tiles = (a.Lk + bn - 1) / bn;
+  if (2 * ctas > slots) return 1;
+  const long long parts = slots / ctas, most = tiles / 4;
+  return (int)(parts < most ? parts : (most < 1 ? 1 : most));
+}
+
 template <class T, int D>
-cudaError_t forward(const BiasAttnArgs& a, cudaStream_t st) {
+cudaError_t forward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
   using C = FwdCfg<D>;
-  static_assert(2 * C::SMEM <= 227 * 1024, "two CTAs per SM");
+  static_assert(2 * (C::SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
   cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const long long grid = (long long)a.B * a.hq * ((a.Lq + 127) / 128);
+  const Split sp = split_of(a, forward_splits(a), scratch);
+  const long long grid = (long long)a.B * a.hq * ((a.Lq + 127) / 128) * sp.n;
   prof_begin(kKindOther, st);
-  attn_fwd_kernel<T, D><<<(unsigned)grid, kFwdThreads, C::SMEM, st>>>(a, Split{1, nullptr, nullptr});
+  attn_fwd_kernel<T, D><<<(unsigned)grid, kFwdThreads, C::SMEM, st>>>(a, sp);
   prof_end(kKindOther, st);
   count_launch();
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e == cudaSuccess && sp.n > 1 ? launch_attention_join<T, D>(a, sp, st) : e;
 }
 
 template <class T>
-cudaError_t forward_d(const BiasAttnArgs& a, cudaStream_t st) {
-  if (a.d == 32) return forward<T, 32>(a, st);
-  if (a.d == 64) return forward<T, 64>(a, st);
-  return forward<T, 128>(a, st);
+cudaError_t forward_d(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
+  if (a.d == 32) return forward<T, 32>(a, scratch, st);
+  if (a.d == 64) return forward<T, 64>(a, scratch, st);
+  return forward<T, 128>(a, scratch, st);
 }
 
 }  // namespace
 
-size_t bias_attention_scratch_bytes(const BiasAttnArgs&) { return 0; }
-cudaError_t launch_bias_attention(const BiasAttnArgs& a, int dtype, void*, cudaStream_t st) {
-  return dtype == kBF16 ? forward_d<__nv_bfloat16>(a, st) : forward_d<__half>(a, st);
+size_t bias_attention_scratch_bytes(const BiasAttnArgs& a) {
+  return split_bytes(a, token_form(a) ? token_splits(a) : forward_splits(a));
+}
+cudaError_t launch_bias_attention(const BiasAttnArgs& a, int dtype, void* scratch, cudaStream_t st) {
+  if (token_form(a)) return launch_token_attention(a, dtype, scratch, st);
+  return dtype == kBF16 ? forward_d<__nv_bfloat16>(a, scratch, st) : forward_d<__half>(a, scratch, st);
 }
 
 }  // namespace vswin
