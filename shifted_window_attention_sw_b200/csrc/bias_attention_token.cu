@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
     for (int x = 0; x < D / 8; ++x)
       *reinterpret_cast<float2*>(so + r * D + 8 * x + 2 * qc) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
     if (qc == 0) {
-      sm[2 * r] = any[e] ? m[e] : -INFINITY;
+      sm[2 * r] = any[e] || l[e] != l[e] ? m[e] : -INFINITY;  // (a row of NaN scores has no maximum)
       sm[2 * r + 1] = l[e];
     }
   }
@@ -268,13 +268,19 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
   float top = -INFINITY;
-  for (int s = lane; s < sp.n; s += 32) top = fmaxf(top, sp.lse[s * rows + r]);
+  bool nan = false;
+  for (int s = lane; s < sp.n; s += 32) {
+    const float lse = sp.lse[s * rows + r];
+    top = fmaxf(top, lse);
+    nan = nan || lse != lse;
+  }
+  nan = __any_sync(0xffffffffu, nan);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float total = 0.f, v[D / 32];
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) v[k] = 0.f;
-  if (top > -INFINITY)
+  if (top > -INFINITY && !nan)
     for (int s = 0; s < sp.n; ++s) {
       const float lse = sp.lse[s * rows + r];
       if (lse == -INFINITY) continue;  // a part without a visible key
@@ -284,11 +290,12 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
       for (int k = 0; k < D / 32; ++k) v[k] = fmaf(w, sp.o[(s * rows + r) * D + lane + 32 * k], v[k]);
     }
   const int i = (int)(r % a.Lq), h = (int)(r / a.Lq % a.hq), b = (int)(r / a.Lq / a.hq);
-  const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
+  if (nan) total = top = __int_as_float(0x7fffffff);
+  const float inv = total > 0.f || nan ? 1.f / total : 0.f;
   T* out = static_cast<T*>(a.o.p) + a.o.at(b, i, h);
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) out[lane + 32 * k] = from_f<T>(v[k] * inv);
-  if (lane == 0) a.lse[r] = top > -INFINITY ? (top + log2f(total)) * kLn2 : -INFINITY;
+  if (lane == 0) a.lse[r] = top > -INFINITY || nan ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
 // Parts of the keys: enough CTAs for four waves of what is resident (sequences

@@ -565,3 +565,22 @@ def test_token_by_token_equals_the_whole_sequence():
         out, _ = vswin.bias_attention_forward(qn, kc, vc, i["table"], i["map"], causal=True, kv_lens=n, q_start=n - 1)
         bound = 2 * (2.0**-8) * (whole[:, t].double().abs() + i["v"][:, :t + 1].double().abs().amax(1).repeat_interleave(2, 1))
         assert ((out[:, 0].double() - whole[:, t].double()).abs() <= bound).all(), t
+
+
+@pytest.mark.parametrize("Lq,Lk", [(150, 150), (1, 150), (1, 5000), (100, 6000)], ids=str)
+def test_attention_nan_stays_in_its_row(Lq, Lk):
+    # a query row of NaN gives a row of NaN and nothing else; a key of NaN reaches the rows that see it
+    ins, _ = _attn_inputs(BF16, 2, Lq, Lk, 2, 2, 64)
+    good = vswin.bias_attention_forward(*ins, _map())
+    q = ins[0].clone()
+    q[1, Lq // 2, 1] = math.nan
+    out, lse = vswin.bias_attention_forward(q, *ins[1:], _map())
+    assert out[1, Lq // 2, 1].isnan().all() and lse[1, 1, Lq // 2].isnan()
+    rest = torch.ones_like(lse, dtype=torch.bool)
+    rest[1, 1, Lq // 2] = False
+    assert torch.equal(lse[rest], good[1][rest])
+    assert torch.equal(out.transpose(1, 2)[rest], good[0].transpose(1, 2)[rest])
+    k = ins[1].clone()
+    k[0, Lk - 1, 0, 3] = math.nan
+    out, lse = vswin.bias_attention_forward(ins[0], k, *ins[2:], _map(), kv_lens=_i32(Lk, Lk - 1))
+    assert out[0, :, 0].isnan().all() and torch.isfinite(out[0, :, 1]).all() and torch.isfinite(out[1]).all()
