@@ -24,9 +24,9 @@
 // bucket (all far ones) skip the line: one value for the whole tile.
 //
 // Softmax in one pass: a tile's P is formed against the row's reference m, the
-// maximum as it was when it last moved. Only when a score exceeds m by more
-// than kSlack (in log2) does the warp raise m and rescale O; P is at most
-// 2^kSlack, exact in fp32 sums and finite in 16 bits, and o and lse do not
+// maximum as it was when it last moved, so that its exponentials do not wait
+// for its maximum. Only when a score exceeds m by more than kSlack (in log2)
+// does the warp raise m, form P again and rescale O; P is at most 2^kSlack, exact in fp32 sums and finite in 16 bits, and o and lse do not
 // depend on m. TMEM columns: scores [0, 64) and [64, 128), O behind.
 //
 // Bound: one exponential per visible pair (16 per clock and SM) for D = 32 and
@@ -75,12 +75,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
   uint64_t* k_free = bars + ST;       // [ST]
   uint64_t* v_full = bars + 2 * ST;   // [ST]
   uint64_t* v_free = bars + 3 * ST;   // [ST]
-  uint64_t* b_full = bars + 4 * ST;   // [ST] bias line
-  uint64_t* b_free = bars + 5 * ST;   // [ST]
-  uint64_t* s_full = bars + 6 * ST;   // [2] scores in TMEM
-  uint64_t* p_full = s_full + 2;      // [2] P written over them
-  uint64_t* o_done = s_full + 4;      // P V accumulated
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_full + 5);
+  uint64_t* s_full = bars + 4 * ST;   // [ST] bias line written and scores in TMEM
+  uint64_t* p_full = bars + 5 * ST;   // [2] P written over them
+  uint64_t* o_done = p_full + 2;      // P V accumulated
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(p_full + 3);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // heavy query tiles (causal: the last) first
@@ -105,13 +103,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
       mbar_init(&k_free[k], 1);
       mbar_init(&v_full[k], kProducers);
       mbar_init(&v_free[k], 1);
-      mbar_init(&b_full[k], kProducers);
-      mbar_init(&b_free[k], kSoftmaxWarps);
+      mbar_init(&s_full[k], kProducers + 1);
     }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(&s_full[k], 1);
-      mbar_init(&p_full[k], kSoftmaxWarps);
-    }
+    for (int k = 0; k < 2; ++k) mbar_init(&p_full[k], kSoftmaxWarps);
     mbar_init(o_done, 1);
     fence_mbar_init();
   }
@@ -142,47 +136,47 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
       if (t >= ST && !warp_wait(&v_free[s], parity, a.ctx, kErrAttnLoad)) break;
       load_tile<T, D, kBn, kProducers>(sv + s * C::kTile, vh, a.v.st, j0, nk, p);
       cp_async_mbar_arrive_noinc(&v_full[s]);
-      if (t >= ST && !warp_wait(&b_free[s], parity, a.ctx, kErrAttnLoad)) break;
       fill_bias_line<T, kLineN, false, kProducers>(&lines[s], a, h, j0 - pos0 - 127, p);
-      mbar_arrive(&b_full[s]);
+      mbar_arrive(&s_full[s]);  // (the line was free when V was)
       if (++s == ST) s = 0, parity ^= 1;
     }
     cp_async_wait_all();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      const uint32_t sq = smem_u32(smem + C::OFF_Q), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
-      constexpr uint32_t id_s = idesc16<T>(128, kBn, 0, 0), id_o = idesc16<T>(128, D, 0, 1);
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return mbar_wait(bar, parity, a.ctx.err, kErrAttnMma, a.ctx.wait_limit);
-      };
-      int ks = 0, vs = 0;
-      uint32_t kp = 0, vp = 0;
-      auto scores = [&](int t) {
-        if (!wait(&k_full[ks], kp)) return false;
-        fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
-        tc_fence_after();
+    // (the whole warp waits, one elected lane issues)
+    const uint32_t sq = smem_u32(smem + C::OFF_Q), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
+    constexpr uint32_t id_s = idesc16<T>(128, kBn, 0, 0), id_o = idesc16<T>(128, D, 0, 1);
+    int ks = 0, vs = 0;
+    uint32_t kp = 0, vp = 0;
+    auto scores = [&](int t) {
+      if (!warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma)) return false;
+      fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
+      tc_fence_after();
+      if (elect_one()) {
         mma_rows<D>(tmem + kBn * (t & 1), sq, sk + ks * C::kTile, id_s);
-        umma_commit(&s_full[t & 1]);
+        umma_commit(&s_full[ks]);
         umma_commit(&k_free[ks]);
-        if (++ks == ST) ks = 0, kp ^= 1;
-        return true;
-      };
-      bool ok = true;
-      for (int t = 0; t < 2 && t < nt && ok; ++t) ok = scores(t);
-      for (int t = 0; t < nt && ok; ++t) {
-        ok = wait(&v_full[vs], vp) && wait(&p_full[t & 1], (t >> 1) & 1);
-        if (!ok) break;
-        fence_proxy_async_smem();
-        tc_fence_after();
+      }
+      __syncwarp();
+      if (++ks == ST) ks = 0, kp ^= 1;
+      return true;
+    };
+    bool ok = true;
+    for (int t = 0; t < 2 && t < nt && ok; ++t) ok = scores(t);
+    for (int t = 0; t < nt && ok; ++t) {
+      ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t & 1], (t >> 1) & 1, a.ctx, kErrAttnMma);
+      if (!ok) break;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      if (elect_one()) {
         mma_acc<D, kBn>(tmem + C::kColO, tmem + kBn * (t & 1), sv + vs * C::kTile, id_o, t == 0);
         umma_commit(o_done);
         umma_commit(&v_free[vs]);
-        if (++vs == ST) vs = 0, vp ^= 1;
-        if (t + 2 < nt) ok = scores(t + 2);  // runs after P V, which reads these columns
       }
+      __syncwarp();
+      if (++vs == ST) vs = 0, vp ^= 1;
+      if (t + 2 < nt) ok = scores(t + 2);  // runs after P V, which reads these columns
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     const uint32_t tw = tmem + ((uint32_t)(warp * 32) << 16);
@@ -195,8 +189,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
     int s = 0;
     uint32_t parity = 0;
     for (int t = 0; t < nt; ++t) {
-      ok = warp_wait(&b_full[s], parity, a.ctx, kErrAttnSoftmax) &&
-           warp_wait(&s_full[t & 1], (t >> 1) & 1, a.ctx, kErrAttnSoftmax);
+      ok = warp_wait(&s_full[s], parity, a.ctx, kErrAttnSoftmax);
       if (!ok) break;
       tc_fence_after();
       const uint32_t buf = tw + kBn * (t & 1);
@@ -232,6 +225,19 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < kBn; ++k) x[k] = k < live ? x[k] : -INFINITY;
       }
+      // P against the reference as it stands, while the maximum is found beside it
+      uint32_t w[kBn / 2];
+      float2 acc;
+      auto form = [&]() {
+        acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kBn; k += 2) {
+          const float2 p = make_float2(ex2(x[k]), ex2(x[k + 1]));
+          acc = __fadd2_rn(acc, p);
+          w[k / 2] = pack2<T>(p.x, p.y);
+        }
+      };
+      form();
       float tops[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
       for (int k = 4; k < kBn; k += 8) {
@@ -247,41 +253,29 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
         l *= alpha;
 #pragma unroll
         for (int k = 0; k < kBn; ++k) x[k] -= shift;
+        form();
         if (t > 0) {
           ok = warp_wait(o_done, (t - 1) & 1, a.ctx, kErrAttnSoftmax);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t w[16];
-            tmem_ld16(tw + C::kColO + c0, w);
-            tmem_wait_ld_keep(w);
+            uint32_t r[16];
+            tmem_ld16(tw + C::kColO + c0, r);
+            tmem_wait_ld_keep(r);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
-            tmem_st16(tw + C::kColO + c0, w);
+            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
+            tmem_st16(tw + C::kColO + c0, r);
           }
         }
       }
-      float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int c0 = 0; c0 < kBn; c0 += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float2 p = make_float2(ex2(x[c0 + k]), ex2(x[c0 + k + 1]));
-          acc = __fadd2_rn(acc, p);
-          w[k / 2] = pack2<T>(p.x, p.y);
-        }
-        tmem_st16(buf + c0 / 2, w);
-      }
+      tmem_st16(buf, w);
+      tmem_st16(buf + 16, w + 16);
       l += acc.x + acc.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&p_full[t & 1]);
-        mbar_arrive(&b_free[s]);
-      }
+      if (lane == 0) mbar_arrive(&p_full[t & 1]);
       if (++s == ST) s = 0, parity ^= 1;
     }
     if (ok && nt > 0) ok = warp_wait(o_done, (nt - 1) & 1, a.ctx, kErrAttnSoftmax);

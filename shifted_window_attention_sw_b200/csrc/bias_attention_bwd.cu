@@ -162,46 +162,42 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     cp_async_wait_all();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0 && nt > 0) {
-      constexpr uint32_t id_s = idesc16<T>(128, kBn, 0, 0), id_acc = idesc16<T>(128, D, 0, 1);
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return mbar_wait(bar, parity, a.ctx.err, kErrAttnMma, a.ctx.wait_limit);
-      };
-      int ss = 0;        // stage and parity of the next scores' tile
-      uint32_t sp = 0;
-      auto scores = [&](int t) {
-        if (!wait(&full[ss], sp)) return false;
-        fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
-        tc_fence_after();
+    // (the whole warp waits, one elected lane issues)
+    constexpr uint32_t id_s = idesc16<T>(128, kBn, 0, 0), id_acc = idesc16<T>(128, D, 0, 1);
+    int ss = 0;  // stage and parity of the next scores' tile
+    uint32_t sp = 0;
+    auto scores = [&](int t) {
+      if (!warp_wait(&full[ss], sp, a.ctx, kErrAttnMma)) return false;
+      fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
+      tc_fence_after();
+      if (elect_one()) {
         const uint32_t buf = tmem + 128 * (t % G), m1 = sm + ss * 2 * C::kMoving;
         mma_rows<D>(buf, sf, m1, id_s);
         mma_rows<D>(buf + 64, sf + C::kFixed, m1 + C::kMoving, id_s);
         umma_commit(&s_full[t % G]);
-        if (++ss == ST) ss = 0, sp ^= 1;
-        return true;
-      };
-      bool ok = wait(f_full, 0);
-      fence_proxy_async_smem();
-      for (int t = 0; t < G && t < nt && ok; ++t) ok = scores(t);
-      int as = 0;
-      for (int t = 0; t < nt && ok; ++t) {
-        ok = wait(&ds_full[t % G], (t / G) & 1);
-        if (!ok) break;
-        tc_fence_after();
+      }
+      __syncwarp();
+      if (++ss == ST) ss = 0, sp ^= 1;
+      return true;
+    };
+    bool ok = nt > 0 && warp_wait(f_full, 0, a.ctx, kErrAttnMma);
+    for (int t = 0; t < G && t < nt && ok; ++t) ok = scores(t);
+    int as = 0;
+    for (int t = 0; t < nt && ok; ++t) {
+      ok = warp_wait(&ds_full[t % G], (t / G) & 1, a.ctx, kErrAttnMma);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
         const uint32_t buf = tmem + 128 * (t % G), m1 = sm + as * 2 * C::kMoving;
-        if (kKeys) {
-          mma_acc<D, kBn>(tmem + C::kColAcc, buf + 64, m1, id_acc, t == 0);                   // dk += dS^T q
-          mma_acc<D, kBn>(tmem + C::kColAcc + D, buf, m1 + C::kMoving, id_acc, t == 0);       // dv += P^T dO
-        } else {
-          mma_acc<D, kBn>(tmem + C::kColAcc, buf + 64, m1, id_acc, t == 0);                   // dq += dS k
-        }
+        mma_acc<D, kBn>(tmem + C::kColAcc, buf + 64, m1, id_acc, t == 0);  // dq += dS k, or dk += dS^T q
+        if (kKeys) mma_acc<D, kBn>(tmem + C::kColAcc + D, buf, m1 + C::kMoving, id_acc, t == 0);  // dv += P^T dO
         umma_commit(&free_[as]);
         if (t == nt - 1) umma_commit(done);
-        if (++as == ST) as = 0;
-        if (t + G < nt) ok = scores(t + G);  // runs after the sums, which read these columns
       }
+      __syncwarp();
+      if (++as == ST) as = 0;
+      if (t + G < nt) ok = scores(t + G);  // runs after the sums, which read these columns
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ P and dS
     const int g = warp >> 2;
