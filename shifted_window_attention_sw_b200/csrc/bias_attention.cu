@@ -14,9 +14,9 @@
 // (fp32), four softmax warps (TMEM lane = query row) turn it into P (16 bits,
 // written over the scores, the A operand of a TS MMA) and O += P V accumulates
 // in TMEM. While the warps work on one tile, P V of the tile before and the
-// scores of the next run. Two producer warps bring K and V tiles (two or three stages)
-// with cp.async, which zero-fills what lies behind the lengths whatever it
-// holds, and prepare each tile's bias.
+// scores of the next run. Two producer warps bring K and V tiles (two or three
+// stages, TMA) and prepare each tile's bias; a tile in which the keys end goes
+// by cp.async instead, so that nothing behind the lengths is read.
 //
 // Bias: it depends on j - i alone, so a tile needs 127 + BN values, one line in
 // shared memory that row i reads from entry 127 - i on (consecutive rows,
@@ -63,8 +63,14 @@ struct FwdCfg {
   static_assert(kColO + D <= 256, "TMEM columns of a CTA");
 };
 
+struct FwdParams {
+  HeadMap q, k, v;
+  BiasAttnArgs a;
+};
+
 template <class T, int D>
-__global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_constant__ BiasAttnArgs a, Split sp) {
+__global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_constant__ FwdParams params, Split sp) {
+  const BiasAttnArgs& a = params.a;
   using C = FwdCfg<D>;
   using Line = typename C::Line;
   constexpr int ST = C::ST;
@@ -78,7 +84,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
   uint64_t* s_full = bars + 4 * ST;   // [ST] bias line written and scores in TMEM
   uint64_t* p_full = bars + 5 * ST;   // [2] P written over them
   uint64_t* o_done = p_full + 2;      // P V accumulated
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(p_full + 3);
+  uint64_t* q_full = p_full + 3;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(p_full + 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // heavy query tiles (causal: the last) first
@@ -99,14 +106,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
 
   if (tid == 0) {
     for (int k = 0; k < ST; ++k) {
-      mbar_init(&k_full[k], kProducers);
+      mbar_init(&k_full[k], kProducerWarps);
       mbar_init(&k_free[k], 1);
-      mbar_init(&v_full[k], kProducers);
+      mbar_init(&v_full[k], kProducerWarps);
       mbar_init(&v_free[k], 1);
-      mbar_init(&s_full[k], kProducers + 1);
+      mbar_init(&s_full[k], kProducerWarps + 1);
     }
     for (int k = 0; k < 2; ++k) mbar_init(&p_full[k], kSoftmaxWarps);
     mbar_init(o_done, 1);
+    mbar_init(q_full, kProducerWarps);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -121,26 +129,20 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
   if (warp > kMmaWarp) {
     // ------------------------------------------------------------ producers
     const int p = tid - 32 * (kMmaWarp + 1);
-    const T* kh = static_cast<const T*>(a.k.p) + a.k.at(b, 0, hk);
-    const T* vh = static_cast<const T*>(a.v.p) + a.v.at(b, 0, hk);
     const uint32_t sq = smem_u32(smem + C::OFF_Q), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
-    if (nt > 0)
-      load_tile<T, D, 128, kProducers>(sq, static_cast<const T*>(a.q.p) + a.q.at(b, 0, h), a.q.st, i0, sl.nq, p);
+    if (nt > 0) bring_tile<T, D, 128>(sq, params.q, a.q, b, h, i0, sl.nq, a.Lq, q_full, p);
     int s = 0;
     uint32_t parity = 1;  // of the stage's previous use
     for (int t = 0; t < nt; ++t) {
       const int j0 = (t0 + t) * kBn;
       if (t >= ST && !warp_wait(&k_free[s], parity, a.ctx, kErrAttnLoad)) break;
-      load_tile<T, D, kBn, kProducers>(sk + s * C::kTile, kh, a.k.st, j0, nk, p);
-      cp_async_mbar_arrive_noinc(&k_full[s]);
+      bring_tile<T, D, kBn>(sk + s * C::kTile, params.k, a.k, b, hk, j0, sl.nk, a.Lk, &k_full[s], p);
       if (t >= ST && !warp_wait(&v_free[s], parity, a.ctx, kErrAttnLoad)) break;
-      load_tile<T, D, kBn, kProducers>(sv + s * C::kTile, vh, a.v.st, j0, nk, p);
-      cp_async_mbar_arrive_noinc(&v_full[s]);
+      bring_tile<T, D, kBn>(sv + s * C::kTile, params.v, a.v, b, hk, j0, sl.nk, a.Lk, &v_full[s], p);
       fill_bias_line<T, kLineN, false, kProducers>(&lines[s], a, h, j0 - pos0 - 127, p);
-      mbar_arrive(&s_full[s]);  // (the line was free when V was)
+      if (lane == 0) mbar_arrive(&s_full[s]);  // (the line was free when V was)
       if (++s == ST) s = 0, parity ^= 1;
     }
-    cp_async_wait_all();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     // (the whole warp waits, one elected lane issues)
@@ -150,10 +152,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
     uint32_t kp = 0, vp = 0;
     auto scores = [&](int t) {
       if (!warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma)) return false;
-      fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
       tc_fence_after();
       if (elect_one()) {
-        mma_rows<D>(tmem + kBn * (t & 1), sq, sk + ks * C::kTile, id_s);
+        mma_rows<D, kBn>(tmem + kBn * (t & 1), sq, sk + ks * C::kTile, id_s);
         umma_commit(&s_full[ks]);
         umma_commit(&k_free[ks]);
       }
@@ -161,12 +162,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
       if (++ks == ST) ks = 0, kp ^= 1;
       return true;
     };
-    bool ok = true;
+    bool ok = nt > 0 && warp_wait(q_full, 0, a.ctx, kErrAttnMma);
     for (int t = 0; t < 2 && t < nt && ok; ++t) ok = scores(t);
     for (int t = 0; t < nt && ok; ++t) {
       ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t & 1], (t >> 1) & 1, a.ctx, kErrAttnMma);
       if (!ok) break;
-      fence_proxy_async_smem();
       tc_fence_after();
       if (elect_one()) {
         mma_acc<D, kBn>(tmem + C::kColO, tmem + kBn * (t & 1), sv + vs * C::kTile, id_o, t == 0);
@@ -342,9 +342,15 @@ cudaError_t forward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const Split sp = split_of(a, forward_splits(a), scratch);
+  const int dtype = std::is_same<T, __half>::value ? kFP16 : kBF16;
+  FwdParams params;
+  params.a = a;
+  make_head_map(&params.q, a.q, a.B, a.Lq, a.hq, D, dtype, 128);
+  make_head_map(&params.k, a.k, a.B, a.Lk, a.hk, D, dtype, kBn);
+  make_head_map(&params.v, a.v, a.B, a.Lk, a.hk, D, dtype, kBn);
   const long long grid = (long long)a.B * a.hq * ((a.Lq + 127) / 128) * sp.n;
   prof_begin(kKindOther, st);
-  attn_fwd_kernel<T, D><<<(unsigned)grid, kFwdThreads, C::SMEM, st>>>(a, sp);
+  attn_fwd_kernel<T, D><<<(unsigned)grid, kFwdThreads, C::SMEM, st>>>(params, sp);
   prof_end(kKindOther, st);
   count_launch();
   e = cudaGetLastError();

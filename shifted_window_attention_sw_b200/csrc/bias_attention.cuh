@@ -1,14 +1,16 @@
 // What the kernels of the attention with bucketed bias share: the lengths and
 // positions of a sequence, the bias of an offset, and the tensor-core tiles.
 //
-// Tiles in shared memory: rows of D channels as 8 x 16-byte core matrices
-// without swizzle, element (row r, channel c) at (r / 8) 16 D + (c / 8) 128 +
-// (r % 8) 16 + (c % 8) 2. The same tile serves as a K-major operand (rows are
-// M or N, channels are K: 128 bytes between 8-channel groups, 16 D between
-// 8-row groups) and as an MN-major one (channels are N, rows are K).
+// Tiles in shared memory: rows in pieces of kPiece channels (64, or 32 for D =
+// 32), a piece's rows one after another (128 or 64 bytes each) with the 16-byte
+// chunk index XORed with the row (its low three bits, or bits 1-2): what TMA
+// writes and the tensor core reads with the 128- or 64-byte swizzle. The same
+// tile serves as a K-major operand (rows are M or N, channels are K) and as an
+// MN-major one (channels are N, rows are K).
 #pragma once
 
 #include <cmath>
+#include <cuda.h>
 
 #include "sequence.h"
 #include "sm100.cuh"
@@ -95,55 +97,110 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, int a_mn, int b_mn)
              : idesc_bf16(M, N, a_mn, b_mn);
 }
 
-// Operand descriptors of a tile of D channels starting at `addr`.
 template <int D>
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {  // channels are K; 16 channels = +256 bytes
-  return smem_desc(addr, 128, 16 * D);
-}
+struct TileOf {
+  static constexpr int kPiece = D == 32 ? 32 : 64;      // channels
+  static constexpr int kRow = kPiece * 2;               // bytes of a row of a piece
+  static constexpr uint64_t kLayout = D == 32 ? 4 : 2;  // 64- or 128-byte swizzle
+  static __device__ __forceinline__ int offset(int rows, int r, int c) {  // of 16-byte chunk c of row r
+    const int piece = c / (kPiece / 8), x = c % (kPiece / 8);
+    return piece * rows * kRow + r * kRow + ((x ^ (D == 32 ? (r >> 1) & 3 : r & 7)) << 4);
+  }
+};
+
+// Operand descriptors: 8-row groups 8 kRow bytes apart. K-major: 16 channels of
+// a piece are 32 bytes further on. MN-major: pieces `lbo` bytes apart, 16 rows
+// are 16 kRow bytes further on.
 template <int D>
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {  // rows are K; 16 rows = +32 D bytes
-  return smem_desc(addr, 16 * D, 128);
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((8 * TileOf<D>::kRow) >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= TileOf<D>::kLayout << 61;
+  return d;
 }
 
-// D[128 x N] (+)= A B^T, both tiles K-major over D channels.
-template <int D>
+// D[128 x ROWS] (+)= A B^T, A a tile of 128 rows, B of ROWS, both K-major.
+template <int D, int ROWS>
 __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr, uint32_t idesc) {
-  const uint64_t da = desc_k<D>(a_addr), db = desc_k<D>(b_addr);
+  using Tl = TileOf<D>;
+  const uint64_t da = tile_desc<D>(a_addr, 16), db = tile_desc<D>(b_addr, 16);
 #pragma unroll
-  for (int k = 0; k < D / 16; ++k) umma_ss(d_tmem, da + 16 * k, db + 16 * k, idesc, k > 0);
+  for (int k = 0; k < D / 16; ++k) {
+    const int piece = 16 * k / Tl::kPiece, in = 16 * k % Tl::kPiece * 2;
+    umma_ss(d_tmem, da + ((piece * 128 * Tl::kRow + in) >> 4), db + ((piece * ROWS * Tl::kRow + in) >> 4), idesc, k > 0);
+  }
 }
 // D[128 x D] (+)= A[128 x ROWS] B, A packed in TMEM (8 columns per 16 rows of B), B a tile of ROWS rows.
 template <int D, int ROWS>
 __device__ __forceinline__ void mma_acc(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_addr, uint32_t idesc, bool first) {
-  const uint64_t db = desc_mn<D>(b_addr);
+  const uint64_t db = tile_desc<D>(b_addr, ROWS * TileOf<D>::kRow);
 #pragma unroll
   for (int k = 0; k < ROWS / 16; ++k)
-    umma_ts(d_tmem, a_tmem + 8 * k, db + (uint64_t)(2 * D * k), idesc, (first && k == 0) ? 0u : 1u);
-}
-
-// cp.async of rows [r0, r0 + ROWS) of a head into a tile; rows outside [0, n)
-// become zeros. `p` of `threads` threads (whole warps); a warp's copy takes 8
-// rows of 4 pieces of 16 bytes (64 contiguous bytes of a row, 128 contiguous
-// bytes of shared memory per 8 lanes).
-template <class T, int D, int ROWS, int THREADS>
-__device__ __forceinline__ void load_tile(uint32_t dst, const T* head, long long row_stride, int r0, int n, int p) {
-  const int r = p & 7, c = (p >> 3) & 3;
-  constexpr int kGroups = ROWS / 8 * (D / 32);  // groups of 8 rows x 32 channels
-#pragma unroll
-  for (int g = 0; g < kGroups; g += THREADS / 32) {
-    const int gi = g + (p >> 5);
-    if (kGroups % (THREADS / 32) != 0 && gi >= kGroups) break;
-    const int rg = gi / (D / 32), cg = gi % (D / 32);
-    const int row = r0 + rg * 8 + r;
-    const bool in = row >= 0 && row < n;
-    const T* src = head + (in ? (long long)row * row_stride : 0) + cg * 32 + c * 8;
-    const uint32_t to = dst + rg * 16 * D + (cg * 4 + c) * 128 + r * 16;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(in ? 16u : 0u) : "memory");
-  }
+    umma_ts(d_tmem, a_tmem + 8 * k, db + (uint64_t)(k * TileOf<D>::kRow), idesc, (first && k == 0) ? 0u : 1u);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Rows of one head of a tensor, by TMA where a map could be made.
+struct HeadMap {
+  CUtensorMap map;    // (channels, tokens, heads, batch)
+  int use;
+  int hmul, bmul;     // 0 for a dimension of stride 0 (its map has one entry)
+};
+
+// cp.async of rows [r0, r0 + ROWS) of a head into a tile; rows outside [0, n)
+// become zeros. `p` of `THREADS` threads (whole warps); a warp's copy takes 8
+// rows of 4 chunks of 16 bytes.
+template <class T, int D, int ROWS, int THREADS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const T* head, long long row_stride, int r0, int n, int p) {
+  const int r = p & 7, c = (p >> 3) & 3;
+  constexpr int kGroups = ROWS / 8 * (D / 32);  // groups of 8 rows x 32 channels
+#pragma unroll 4
+  for (int g = p >> 5; g < kGroups; g += THREADS / 32) {
+    const int at = g / (D / 32) * 8 + r, chunk = g % (D / 32) * 4 + c;
+    const int row = r0 + at;
+    const bool in = row >= 0 && row < n;
+    const T* src = head + (in ? (long long)row * row_stride : 0) + chunk * 8;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + TileOf<D>::offset(ROWS, at, chunk)), "l"(src),
+                 "r"(in ? 16u : 0u)
+                 : "memory");
+  }
+}
+
+// Rows [r0, r0 + ROWS) of head h of sequence b into a tile, by two producer
+// warps (p: thread of the 64), whose leaders' arrivals complete `bar` (count 2)
+// with the copies. n of the L rows take part: whole tiles go by TMA (which
+// reads zeros behind L); a tile in which the length ends goes by cp.async,
+// which reads nothing behind it, whatever it holds.
+template <class T, int D, int ROWS>
+__device__ __forceinline__ void bring_tile(uint32_t dst, const HeadMap& m, const Heads& v, int b, int h, int r0, int n,
+                                           int L, uint64_t* bar, int p) {
+  using Tl = TileOf<D>;
+  if (m.use && (r0 + ROWS <= n || n == L)) {
+    if (p == 0) {
+      mbar_arrive_expect_tx(bar, ROWS * D * 2);
+#pragma unroll
+      for (int c = 0; c < D; c += Tl::kPiece)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+            "%5}], [%6];" ::"r"(dst + c / Tl::kPiece * ROWS * Tl::kRow),
+            "l"(reinterpret_cast<uint64_t>(&m.map)), "r"(c), "r"(r0), "r"(h * m.hmul), "r"(b * m.bmul), "r"(smem_u32(bar))
+            : "memory");
+    } else if (p == 32) {
+      mbar_arrive(bar);
+    }
+  } else {
+    load_tile<T, D, ROWS, 64>(dst, static_cast<const T*>(v.p) + v.at(b, 0, h), v.st, r0, n, p);
+    cp_async_wait_all();
+    fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
+    __syncwarp();
+    if ((p & 31) == 0) mbar_arrive(bar);
+  }
 }
 
 // A whole warp waits; false in every lane when any lane's wait gave up.
@@ -208,6 +265,11 @@ __device__ __forceinline__ void fill_bias_line(BiasLine<N, kBuckets>* o, const B
     o->value = first;
     o->which = which;
   }
+  __syncwarp();  // a leader's arrival stands for its warp
 }
+
+// Map of a tensor of B x L x H rows of d channels in boxes of `rows` rows; false
+// (m->use = 0) when its strides have no map.
+bool make_head_map(HeadMap* m, const Heads& v, int B, int L, int H, int d, int dtype, int rows);
 
 }  // namespace vswin

@@ -53,6 +53,7 @@ struct BwdCfg {
 };
 
 struct BwdArgs {
+  HeadMap f1, f2, m1, m2;  // of the fixed and moving tiles
   BiasAttnArgs a;
   float* delta;    // [B][hq][Lq] D
   float* dtab;     // [hq][B * query tiles][buckets] shares of the table's gradient
@@ -102,14 +103,14 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
 
   if (tid == 0) {
     for (int k = 0; k < ST; ++k) {
-      mbar_init(&full[k], 2 * kProducers);
+      mbar_init(&full[k], 3 * 2);
       mbar_init(&free_[k], 1 + 4);
     }
     for (int k = 0; k < G; ++k) {
       mbar_init(&s_full[k], 1);
       mbar_init(&ds_full[k], 4);
     }
-    mbar_init(f_full, kProducers);
+    mbar_init(f_full, 2 * 2);
     mbar_init(done, 1);
     fence_mbar_init();
   }
@@ -127,11 +128,11 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     // ------------------------------------------------------------ producers
     const int p = tid - 32 * (kMmaWarp + 1);
     const Heads &F1 = kKeys ? a.k : a.q, &F2 = kKeys ? a.v : a.dout, &M1 = kKeys ? a.q : a.k, &M2 = kKeys ? a.dout : a.v;
-    const int fn = kKeys ? sl.nk : sl.nq;
+    const int fn = kKeys ? sl.nk : sl.nq, fL = kKeys ? a.Lk : a.Lq;
+    const int mn = kKeys ? sl.nq : sl.nk, mL = kKeys ? a.Lq : a.Lk;
     if (nt > 0) {
-      load_tile<T, D, 128, kProducers>(sf, static_cast<const T*>(F1.p) + F1.at(b, 0, hf), F1.st, f0, fn, p);
-      load_tile<T, D, 128, kProducers>(sf + C::kFixed, static_cast<const T*>(F2.p) + F2.at(b, 0, hf), F2.st, f0, fn, p);
-      cp_async_mbar_arrive_noinc(f_full);
+      bring_tile<T, D, 128>(sf, args.f1, F1, b, hf, f0, fn, fL, f_full, p);
+      bring_tile<T, D, 128>(sf + C::kFixed, args.f2, F2, b, hf, f0, fn, fL, f_full, p);
     }
     int s = 0, u = 0, r0 = m_lo, h = kKeys ? hk * group : hf;
     uint32_t parity = 1;  // of the stage's previous use
@@ -139,9 +140,8 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
       if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad)) break;
       const int hm = kKeys ? h : hk;
       const uint32_t dst = sm + s * 2 * C::kMoving;
-      load_tile<T, D, kBn, kProducers>(dst, static_cast<const T*>(M1.p) + M1.at(b, 0, hm), M1.st, r0, m_hi, p);
-      load_tile<T, D, kBn, kProducers>(dst + C::kMoving, static_cast<const T*>(M2.p) + M2.at(b, 0, hm), M2.st, r0, m_hi, p);
-      cp_async_mbar_arrive_noinc(&full[s]);
+      bring_tile<T, D, kBn>(dst, args.m1, M1, b, hm, r0, mn, mL, &full[s], p);
+      bring_tile<T, D, kBn>(dst + C::kMoving, args.m2, M2, b, hm, r0, mn, mL, &full[s], p);
       if constexpr (kKeys) {
         float2 c = make_float2(-INFINITY, 0.f);  // a query that takes no part: P = 0
         if (r0 + p < m_hi) {
@@ -149,17 +149,16 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
           const float lse = a.lse[r];
           if (lse != -INFINITY) c = make_float2(-lse * kLog2E, -args.delta[r]);
         }
-        cols[s * kBn + p] = c;
+        cols[s * kBn + p] = c;  // (fill_bias_line syncs the warp)
         fill_bias_line<T, kLineN, false, kProducers>(&lines[s], a, h, f0 - (sl.start + r0) - (kBn - 1), p);
       } else {
         fill_bias_line<T, kLineN, true, kProducers>(&lines[s], a, h, r0 - (sl.start + f0) - 127, p);
       }
-      mbar_arrive(&full[s]);
+      if (lane == 0) mbar_arrive(&full[s]);
       if (++s == ST) s = 0, parity ^= 1;
       r0 += kBn;
       if (++u == per_head) u = 0, r0 = m_lo, ++h;
     }
-    cp_async_wait_all();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     // (the whole warp waits, one elected lane issues)
@@ -168,12 +167,11 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     uint32_t sp = 0;
     auto scores = [&](int t) {
       if (!warp_wait(&full[ss], sp, a.ctx, kErrAttnMma)) return false;
-      fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
       tc_fence_after();
       if (elect_one()) {
         const uint32_t buf = tmem + 128 * (t % G), m1 = sm + ss * 2 * C::kMoving;
-        mma_rows<D>(buf, sf, m1, id_s);
-        mma_rows<D>(buf + 64, sf + C::kFixed, m1 + C::kMoving, id_s);
+        mma_rows<D, kBn>(buf, sf, m1, id_s);
+        mma_rows<D, kBn>(buf + 64, sf + C::kFixed, m1 + C::kMoving, id_s);
         umma_commit(&s_full[t % G]);
       }
       __syncwarp();
@@ -435,7 +433,7 @@ __global__ void __launch_bounds__(256) attn_dtable_kernel(const float* dtab, int
 }
 
 template <class T, int D, bool kKeys>
-cudaError_t pass(const BwdArgs& args, cudaStream_t st) {
+cudaError_t pass(BwdArgs& args, cudaStream_t st) {
   using C = BwdCfg<D, kKeys>;
   const BiasAttnArgs& a = args.a;
   const int smem = C::OFF_BINS + (kKeys ? 0 : 4 * C::G * a.buckets * 4);
@@ -443,6 +441,14 @@ cudaError_t pass(const BwdArgs& args, cudaStream_t st) {
   static_assert(C::CTAS * (kMost + 1024) <= 228 * 1024, "shared memory of an SM");
   cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<T, D, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   if (e != cudaSuccess) return e;
+  const int dtype = std::is_same<T, __half>::value ? kFP16 : kBF16;
+  auto map = [&](HeadMap* m, const Heads& v, bool keys, int rows) {
+    make_head_map(m, v, a.B, keys ? a.Lk : a.Lq, keys ? a.hk : a.hq, D, dtype, rows);
+  };
+  map(&args.f1, kKeys ? a.k : a.q, kKeys, 128);
+  map(&args.f2, kKeys ? a.v : a.dout, kKeys, 128);
+  map(&args.m1, kKeys ? a.q : a.k, !kKeys, kBn);
+  map(&args.m2, kKeys ? a.dout : a.v, !kKeys, kBn);
   const long long grid = (long long)a.B * (kKeys ? a.hk : a.hq) * (((kKeys ? a.Lk : a.Lq) + 127) / 128);
   prof_begin(kKindAttnBwd, st);
   attn_bwd_kernel<T, D, kKeys><<<(unsigned)grid, C::THREADS, smem, st>>>(args);
@@ -455,7 +461,10 @@ size_t delta_bytes(const BiasAttnArgs& a) { return ((size_t)a.B * a.hq * a.Lq * 
 
 template <class T, int D>
 cudaError_t backward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
-  BwdArgs args{a, static_cast<float*>(scratch), reinterpret_cast<float*>(static_cast<char*>(scratch) + delta_bytes(a))};
+  BwdArgs args;
+  args.a = a;
+  args.delta = static_cast<float*>(scratch);
+  args.dtab = reinterpret_cast<float*>(static_cast<char*>(scratch) + delta_bytes(a));
   cudaError_t e = pass<T, D, false>(args, st);
   if (e == cudaSuccess) e = pass<T, D, true>(args, st);
   if (e != cudaSuccess) return e;

@@ -9,8 +9,8 @@
 // (16 rows; at so few rows tcgen05's 128 would be seven eighths empty, and the
 // copies are the bound either way) and keeps its own running maximum, sum and
 // O; the warps' results join in shared memory, the key parts' in
-// attn_join_kernel. The pieces are 8 x 16-byte core matrices, which ldmatrix
-// reads without bank conflicts.
+// attn_join_kernel. The pieces are swizzled tiles, which cp.async writes and
+// ldmatrix reads without bank conflicts.
 #include "bias_attention.cuh"
 #include "bias_attention_split.h"
 
@@ -136,11 +136,11 @@ __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
     const uint32_t at = ring + (n % C::ST) * 2 * C::kTile;
     float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     // lanes 8 x .. 8 x + 7 address matrix x: channels 8 (2 k + x % 2).. of keys 8 (x / 2)..
-    const uint32_t kaddr = at + (lane >> 4) * 16 * D + ((lane >> 3) & 1) * 128 + (lane & 7) * 16;
+    const int krow = (lane >> 4) * 8 + (lane & 7), kchunk = (lane >> 3) & 1;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       uint32_t f[4];
-      ldmatrix4(f, kaddr + 256 * k);
+      ldmatrix4(f, at + TileOf<D>::offset(kPiece, krow, 2 * k + kchunk));
       mma16<T>(s[0], qf[k], f[0], f[1]);
       mma16<T>(s[1], qf[k], f[2], f[3]);
     }
@@ -185,11 +185,11 @@ __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
         pf[2 * t + e] = pack2<T>(p0, p1);
       }
     // lanes of matrix x: keys 8 (x % 2).., channels 8 (2 y + x / 2)..
-    const uint32_t vaddr = at + C::kTile + ((lane >> 3) & 1) * 16 * D + (lane >> 4) * 128 + (lane & 7) * 16;
+    const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vchunk = lane >> 4;
 #pragma unroll
     for (int y = 0; y < D / 16; ++y) {
       uint32_t f[4];
-      ldmatrix4_t(f, vaddr + 256 * y);
+      ldmatrix4_t(f, at + C::kTile + TileOf<D>::offset(kPiece, vrow, 2 * y + vchunk));
       mma16<T>(o[2 * y], pf, f[0], f[1]);
       mma16<T>(o[2 * y + 1], pf, f[2], f[3]);
     }
