@@ -123,22 +123,56 @@ __device__ __forceinline__ void store_codes(void* p, bool vec, long long i, long
     if (i + k < n) b[i + k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
 }
 
-__device__ __forceinline__ float decode_m(int c, float s) {
-  const float x = (float)c * (1.f / 127.f);
+// Byte k of w as a float, and back: 2^23 + n has n in its low bits, so a byte
+// permutation and one addition convert (the conversion instructions run at a
+// quarter of the rate).
+__device__ __forceinline__ float byte_float(uint32_t w, int k) {
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + k)) - 8388608.f;
+}
+__device__ __forceinline__ uint32_t round_byte(float x) { return __float_as_uint(x + 12582912.f); }  // low byte: rint(x)
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// Signed codes come as bytes with the sign bit flipped (code + 128).
+__device__ __forceinline__ float decode_m(uint32_t w, int k, float s) {
+  const float x = (byte_float(w, k) - 128.f) * (1.f / 127.f);
   return s * x * fabsf(x);
 }
-__device__ __forceinline__ float decode_v(int c, float s) {
-  const float x = (float)c * (1.f / 255.f);
+__device__ __forceinline__ float decode_v(uint32_t w, int k, float s) {
+  const float x = byte_float(w, k) * (1.f / 255.f);
   const float x2 = x * x;
   return s * (x2 * x2);
 }
+constexpr uint32_t kFlip = 0x80808080u;
 
-// The largest value of a warp, a NaN anywhere making it NaN (so that the block
-// reads back as NaN and is not silently lost).
-__device__ __forceinline__ float warp_max_nan(float x, bool nan) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return __any_sync(0xffffffffu, nan) ? __int_as_float(0x7fffffff) : x;
+// Hardware square roots, within 2 units of the last place.
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sqrt_flush(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Largest magnitudes, a NaN anywhere making them NaN (so that its block reads
+// back as NaN and is not silently lost).
+__device__ __forceinline__ float max3_nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+__device__ __forceinline__ float warp_max_nan(float x) {
+  float r;
+  asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <int kCap, int kBits>
@@ -182,16 +216,18 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       const float sm = t.ms[i / kAdamwBlock], sv = t.vs[i / kAdamwBlock];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        m[k] = decode_m((int)(int8_t)((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))), sm);
-        v[k] = decode_v((int)(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u), sv);
+        m[k] = decode_m((k < 4 ? cm.x : cm.y) ^ kFlip, k & 3, sm);
+        v[k] = decode_v(k < 4 ? cv.x : cv.y, k & 3, sv);
       }
     }
+    float root[8];  // sqrt(v)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float gr = g[k] * gs;
       m[k] = h.b1 * m[k] + h.c1 * gr;
       v[k] = h.b2 * v[k] + h.c2 * (gr * gr);
-      p[k] = t.keep * p[k] - step_size * (m[k] / (sqrtf(v[k]) * inv_bc2 + h.eps));
+      root[k] = sqrt_fast(v[k]);
+      p[k] = t.keep * p[k] - step_size * m[k] * rcp_fast(root[k] * inv_bc2 + h.eps);
     }
     if (t.master) store_elems(t.master, kF32, vec, i, n, p);
     store_elems(t.p, t.p_type, vec, i, n, p);
@@ -199,29 +235,21 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       store_elems(t.m, kF32, vec, i, n, m);
       store_elems(t.v, kF32, vec, i, n, v);
     } else {
-      float am = 0.f, av = 0.f;
-      bool nan_m = false, nan_v = false;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {  // elements behind the tensor are zero here
-        am = fmaxf(am, fabsf(m[k]));
-        av = fmaxf(av, v[k]);
-        nan_m |= m[k] != m[k];
-        nan_v |= v[k] != v[k];
-      }
-      const float sm = warp_max_nan(am, nan_m), sv = warp_max_nan(av, nan_v);
-      const float im = sm > 0.f ? 1.f / sm : 0.f, iv = sv > 0.f ? 1.f / sv : 0.f;
-      uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+      // (elements behind the tensor are zero here)
+      const float sm = warp_max_nan(max3_nan(max3_nan(m[0], m[1], m[2]), max3_nan(m[3], m[4], m[5]), max3_nan(m[6], m[7], 0.f)));
+      const float sv = warp_max_nan(max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), max3_nan(v[6], v[7], 0.f)));
+      // code = 127 sqrt(|m| / s), 255 sqrt(sqrt(v) / sqrt(s)); blocks below 2^-100 have no use for codes, and 1 / s no overflow
+      const float im = sm >= 0x1p-100f ? 127.f * 127.f / sm : 0.f;
+      const float iv = sv >= 0x1p-100f ? 255.f * 255.f * rsqrtf(sv) : 0.f;
+      uint32_t cm[8], cv[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        // the clamps matter where 1 / s overflows (s below 2^-128)
-        const int a = (int)fminf(rintf(sqrtf(fabsf(m[k]) * im) * 127.f), 127.f);
-        int b = (int)fminf(rintf(sqrtf(sqrtf(v[k] * iv)) * 255.f), 255.f);
-        b = v[k] > 0.f && b < 1 ? 1 : b;
-        cm[k >> 2] |= (uint32_t)((m[k] < 0.f ? -a : a) & 255) << (8 * (k & 3));
-        cv[k >> 2] |= (uint32_t)(b & 255) << (8 * (k & 3));
+        const float c = sqrt_flush(root[k] * iv);
+        cm[k] = round_byte(copysignf(sqrt_flush(fabsf(m[k]) * im), m[k]));
+        cv[k] = round_byte(v[k] > 0.f ? fmaxf(c, 1.f) : c);
       }
-      store_codes(t.m, vec, i, n, make_uint2(cm[0], cm[1]));
-      store_codes(t.v, vec, i, n, make_uint2(cv[0], cv[1]));
+      store_codes(t.m, vec, i, n, make_uint2(pack_bytes(cm[0], cm[1], cm[2], cm[3]), pack_bytes(cm[4], cm[5], cm[6], cm[7])));
+      store_codes(t.v, vec, i, n, make_uint2(pack_bytes(cv[0], cv[1], cv[2], cv[3]), pack_bytes(cv[4], cv[5], cv[6], cv[7])));
       if (lane == 0) {
         t.ms[i / kAdamwBlock] = sm;
         t.vs[i / kAdamwBlock] = sv;
@@ -230,21 +258,34 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   }
 }
 
+// Sixteen elements a thread, so that 32 bytes of codes are in flight.
+template <int kType>
 __global__ void __launch_bounds__(kThreads) adamw_decode_kernel(const int8_t* m, const float* ms, const uint8_t* v,
-                                                               const float* vs, long long n, int dtype, bool vec,
-                                                               void* mo, void* vo) {
-  for (long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * 8; i < n;
-       i += (long long)gridDim.x * kThreads * 8) {
-    const uint2 cm = load_codes(m, vec, i, n), cv = load_codes(v, vec, i, n);
-    const float sm = ms[i / kAdamwBlock], sv = vs[i / kAdamwBlock];
+                                                               const float* vs, long long n, bool vec, void* mo, void* vo) {
+  const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * 16;
+  if (i >= n) return;
+  const float sm = ms[i / kAdamwBlock], sv = vs[i / kAdamwBlock];
+  uint4 cm, cv;
+  if (vec && i + 16 <= n) {
+    cm = *reinterpret_cast<const uint4*>(m + i);
+    cv = *reinterpret_cast<const uint4*>(v + i);
+  } else {
+    const uint2 a = load_codes(m, false, i, n), b = load_codes(m, false, i + 8, n);
+    const uint2 c = load_codes(v, false, i, n), d = load_codes(v, false, i + 8, n);
+    cm = make_uint4(a.x, a.y, b.x, b.y);
+    cv = make_uint4(c.x, c.y, d.x, d.y);
+  }
+  const uint32_t wm[4] = {cm.x ^ kFlip, cm.y ^ kFlip, cm.z ^ kFlip, cm.w ^ kFlip}, wv[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
     float fm[8], fv[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      fm[k] = decode_m((int)(int8_t)((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))), sm);
-      fv[k] = decode_v((int)(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u), sv);
+      fm[k] = decode_m(wm[2 * e + k / 4], k & 3, sm);
+      fv[k] = decode_v(wv[2 * e + k / 4], k & 3, sv);
     }
-    store_elems(mo, dtype, vec, i, n, fm);
-    store_elems(vo, dtype, vec, i, n, fv);
+    store_elems(mo, kType, vec, i + 8 * e, n, fm);
+    store_elems(vo, kType, vec, i + 8 * e, n, fv);
   }
 }
 
@@ -291,10 +332,16 @@ cudaError_t launch_adamw_decode(const int8_t* m, const float* ms, const uint8_t*
   if (n == 0) return cudaSuccess;
   const uintptr_t all = reinterpret_cast<uintptr_t>(m) | reinterpret_cast<uintptr_t>(v) |
                         reinterpret_cast<uintptr_t>(m_out) | reinterpret_cast<uintptr_t>(v_out);
-  const long long need = (n + kChunk - 1) / kChunk, cap = (long long)sm_count() * 8;
+  const bool vec = all % 16 == 0;
+  const long long blocks = (n + 16 * kThreads - 1) / (16 * kThreads);
+  if (blocks > 2147483647LL) return cudaErrorInvalidConfiguration;
   prof_begin(kKindOther, st);
-  adamw_decode_kernel<<<(int)(need < cap ? need : cap), kThreads, 0, st>>>(m, ms, v, vs, n, dtype, all % 16 == 0,
-                                                                          m_out, v_out);
+  if (dtype == kBF16)
+    adamw_decode_kernel<kBF16><<<(unsigned)blocks, kThreads, 0, st>>>(m, ms, v, vs, n, vec, m_out, v_out);
+  else if (dtype == kFP16)
+    adamw_decode_kernel<kFP16><<<(unsigned)blocks, kThreads, 0, st>>>(m, ms, v, vs, n, vec, m_out, v_out);
+  else
+    adamw_decode_kernel<kF32><<<(unsigned)blocks, kThreads, 0, st>>>(m, ms, v, vs, n, vec, m_out, v_out);
   prof_end(kKindOther, st);
   count_launch();
   return cudaGetLastError();

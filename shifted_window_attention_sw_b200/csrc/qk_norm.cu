@@ -15,10 +15,11 @@
 // Both directions are bound by HBM: forward reads x and writes y once, backward
 // reads x and dy and writes dx. Vector path: a row is held by d/16 lanes, each
 // with 16 channels as eight (a, b) pairs in registers, so that the rotation
-// needs no exchange between lanes; consecutive lanes take consecutive rows, and
-// two rows per lane are in flight. Rows whose width, alignment or rotation does
-// not split into 16-byte pieces (the rule is vec_ok) go one row per warp,
-// element by element.
+// needs no exchange between lanes. A block takes a few whole tokens at a time,
+// consecutive lanes consecutive heads, and walks the tokens: a lane keeps its
+// head and its gamma, and a position advances by additions alone. Rows whose
+// width, alignment or rotation does not split into 16-byte pieces (the rule is
+// vec_ok) go one row per warp, element by element.
 #include "sequence.h"
 
 namespace vswin {
@@ -65,18 +66,17 @@ __device__ __forceinline__ long long angle_row(const QkNormArgs& a, int b, int l
   return pos;
 }
 
-// Channels of lane t of a row: two runs of 8, and whether its pairs turn.
+// Channels of lane t of a row: two runs of 8, and the first of its eight angles (or -1).
 struct LaneChannels {
   int c0, c1;
-  int angle;  // first of its eight angles, or -1
-  bool inter;
+  int angle;
 };
+template <bool kInter>
 __device__ __forceinline__ LaneChannels lane_channels(const QkNormArgs& a, int t) {
   LaneChannels c;
-  c.inter = a.interleaved != 0;
   const int turned = a.rot / 16;
   c.angle = t < turned ? 8 * t : -1;
-  if (!c.inter && t < turned) {
+  if (!kInter && t < turned) {
     c.c0 = 8 * t;
     c.c1 = 8 * t + a.rot / 2;
   } else {
@@ -87,32 +87,36 @@ __device__ __forceinline__ LaneChannels lane_channels(const QkNormArgs& a, int t
 }
 
 // The two runs as pairs: (a, b) = (run 0, run 1), or even and odd channels.
-__device__ __forceinline__ void to_pairs(const LaneChannels& c, float (&a)[8], float (&b)[8]) {
-  if (!c.inter) return;
-  float x[16];
+template <bool kInter>
+__device__ __forceinline__ void to_pairs(float (&a)[8], float (&b)[8]) {
+  if constexpr (kInter) {
+    float x[16];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    x[k] = a[k];
-    x[8 + k] = b[k];
-  }
+    for (int k = 0; k < 8; ++k) {
+      x[k] = a[k];
+      x[8 + k] = b[k];
+    }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    a[k] = x[2 * k];
-    b[k] = x[2 * k + 1];
+    for (int k = 0; k < 8; ++k) {
+      a[k] = x[2 * k];
+      b[k] = x[2 * k + 1];
+    }
   }
 }
-__device__ __forceinline__ void from_pairs(const LaneChannels& c, float (&a)[8], float (&b)[8]) {
-  if (!c.inter) return;
-  float x[16];
+template <bool kInter>
+__device__ __forceinline__ void from_pairs(float (&a)[8], float (&b)[8]) {
+  if constexpr (kInter) {
+    float x[16];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    x[2 * k] = a[k];
-    x[2 * k + 1] = b[k];
-  }
+    for (int k = 0; k < 8; ++k) {
+      x[2 * k] = a[k];
+      x[2 * k + 1] = b[k];
+    }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    a[k] = x[k];
-    b[k] = x[8 + k];
+    for (int k = 0; k < 8; ++k) {
+      a[k] = x[k];
+      b[k] = x[8 + k];
+    }
   }
 }
 
@@ -140,119 +144,131 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Rows are numbered (b * L + l) * heads + h. The first `qblocks` blocks walk
-// q's rows, the others k's.
-template <class T, int G, bool kBackward>
-__global__ void __launch_bounds__(kThreads) qk_norm_vec_kernel(QkNormArgs a, int qblocks, float* partial) {
+// Tokens of a block's step: whole tokens, a group of G lanes per row; all heads
+// of one token in turns when they outnumber the groups.
+template <int G>
+__host__ __device__ __forceinline__ int tokens_per_step(int heads) {
+  return kThreads / G / heads > 0 ? kThreads / G / heads : 1;
+}
+
+// The first `qblocks` blocks walk q's tokens, the others k's.
+template <class T, int G, bool kBackward, bool kInter>
+__global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
+    qk_norm_vec_kernel(const __grid_constant__ QkNormArgs a, int qblocks, float* partial) {
   const int w = blockIdx.x < qblocks ? 0 : 1;
   const int block = w ? blockIdx.x - qblocks : blockIdx.x;
   const int blocks = w ? gridDim.x - qblocks : qblocks;
   const int heads = a.heads[w];
-  const long long rows = (long long)a.B * a.L * heads;
-  const int t = threadIdx.x % G;
-  const bool live = t < a.d / 16;
-  const LaneChannels c = lane_channels(a, t);
+  const int groups = kThreads / G, per = tokens_per_step<G>(heads), hpb = heads < groups ? heads : groups;
+  const int t = threadIdx.x % G, g = threadIdx.x / G;
+  const bool live = t < a.d / 16 && g / hpb < per;
+  const LaneChannels c = lane_channels<kInter>(a, t);
   const float inv_d = 1.f / (float)a.d;
-  Vec8<T> g0, g1;
+  float ga[8], gb[8], cs[8], sn[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) ga[k] = gb[k] = 0.f, cs[k] = 1.f, sn[k] = 0.f;
   if (live) {
+    Vec8<T> g0, g1;
     load8(static_cast<const T*>(a.gamma[w]) + c.c0, g0);
     load8(static_cast<const T*>(a.gamma[w]) + c.c1, g1);
+    unpack8(g0, ga);
+    unpack8(g1, gb);
+    to_pairs<kInter>(ga, gb);
   }
   float sum_a[8], sum_b[8];
   if (kBackward) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum_a[k] = sum_b[k] = 0.f;
   }
-  const long long per = kThreads / G;  // rows of a block's step
+  // token first + n * step of the walk is token l of sequence b
+  const long long tokens = (long long)a.B * a.L;
+  const long long first = (long long)block * per;
+  const int step = blocks * per, step_b = step / a.L, step_l = step % a.L;
+  int b = (int)((first + g / hpb) / a.L), l = (int)((first + g / hpb) % a.L);
   // every lane of a warp makes the same number of turns (the sums below are warp-wide)
-  for (long long r0 = (long long)block * per; r0 < rows; r0 += (long long)blocks * per) {
-    const long long row = r0 + threadIdx.x / G;
-    const bool on = live && row < rows;
-    int b = 0, l = 0, h = 0;
-    if (row < rows) {
-      const unsigned tok = (unsigned)((unsigned long long)row < (1ull << 32) ? (unsigned)row / (unsigned)heads
-                                                                             : (unsigned long long)row / heads);
-      h = (int)(row - (long long)tok * heads);
-      b = (int)(tok / (unsigned)a.L);
-      l = (int)(tok - (unsigned)b * (unsigned)a.L);
-    }
-    float xa[8], xb[8], ya[8], yb[8], cs[8], sn[8], ga[8], gb[8];
+  for (long long n = first; n < tokens; n += step) {
+    const bool here = live && n + g / hpb < tokens;
+    if (here && c.angle >= 0) load_angles(a, c, angle_row(a, b, l), cs, sn);
+    for (int h0 = 0; h0 < heads; h0 += hpb) {
+      const int h = h0 + g % hpb;
+      const bool on = here && h < heads;
+      float xa[8], xb[8], ya[8], yb[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) xa[k] = xb[k] = ya[k] = yb[k] = 0.f;
-    if (on) {
-      const T* xp = static_cast<const T*>(a.x[w].p) + a.x[w].at(b, l, h);
-      Vec8<T> u0, u1, d0, d1;
-      load8(xp + c.c0, u0);
-      load8(xp + c.c1, u1);
-      if (kBackward) {
-        const T* yp = static_cast<const T*>(a.y[w].p) + a.y[w].at(b, l, h);
-        load8(yp + c.c0, d0);
-        load8(yp + c.c1, d1);
-      }
-      load_angles(a, c, c.angle >= 0 ? angle_row(a, b, l) : 0, cs, sn);
-      unpack8(u0, xa);
-      unpack8(u1, xb);
-      to_pairs(c, xa, xb);
-      if (kBackward) {
-        unpack8(d0, ya);
-        unpack8(d1, yb);
-        to_pairs(c, ya, yb);
-      }
-      unpack8(g0, ga);
-      unpack8(g1, gb);
-      to_pairs(c, ga, gb);
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(xa[k], xa[k], fmaf(xb[k], xb[k], ss));
-    const float r = rsqrtf(group_sum<G>(ss) * inv_d + a.eps);
-    if (!kBackward) {
+      for (int k = 0; k < 8; ++k) xa[k] = xb[k] = ya[k] = yb[k] = 0.f;
       if (on) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float na = xa[k] * r * ga[k], nb = xb[k] * r * gb[k];
-          ya[k] = na * cs[k] - nb * sn[k];
-          yb[k] = nb * cs[k] + na * sn[k];
+        const T* xp = static_cast<const T*>(a.x[w].p) + a.x[w].at(b, l, h);
+        Vec8<T> u0, u1, d0, d1;
+        load8(xp + c.c0, u0);
+        load8(xp + c.c1, u1);
+        if (kBackward) {
+          const T* yp = static_cast<const T*>(a.y[w].p) + a.y[w].at(b, l, h);
+          load8(yp + c.c0, d0);
+          load8(yp + c.c1, d1);
         }
-        from_pairs(c, ya, yb);
-        T* yp = static_cast<T*>(a.y[w].p) + a.y[w].at(b, l, h);
-        store8(yp + c.c0, ya);
-        store8(yp + c.c1, yb);
-      }
-    } else {
-      float along = 0.f;
-      if (on) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float gya = ya[k] * cs[k] + yb[k] * sn[k];  // R^T dy
-          const float gyb = yb[k] * cs[k] - ya[k] * sn[k];
-          xa[k] *= r;
-          xb[k] *= r;
-          sum_a[k] = fmaf(gya, xa[k], sum_a[k]);
-          sum_b[k] = fmaf(gyb, xb[k], sum_b[k]);
-          ya[k] = gya * ga[k];
-          yb[k] = gyb * gb[k];
-          along = fmaf(ya[k], xa[k], fmaf(yb[k], xb[k], along));
+        unpack8(u0, xa);
+        unpack8(u1, xb);
+        to_pairs<kInter>(xa, xb);
+        if (kBackward) {
+          unpack8(d0, ya);
+          unpack8(d1, yb);
+          to_pairs<kInter>(ya, yb);
         }
       }
-      along = group_sum<G>(along) * inv_d;
-      if (on) {
+      float ss = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          ya[k] = r * (ya[k] - xa[k] * along);
-          yb[k] = r * (yb[k] - xb[k] * along);
+      for (int k = 0; k < 8; ++k) ss = fmaf(xa[k], xa[k], fmaf(xb[k], xb[k], ss));
+      const float r = rsqrtf(group_sum<G>(ss) * inv_d + a.eps);
+      if (!kBackward) {
+        if (on) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float na = xa[k] * r * ga[k], nb = xb[k] * r * gb[k];
+            ya[k] = na * cs[k] - nb * sn[k];
+            yb[k] = nb * cs[k] + na * sn[k];
+          }
+          from_pairs<kInter>(ya, yb);
+          T* yp = static_cast<T*>(a.y[w].p) + a.y[w].at(b, l, h);
+          store8(yp + c.c0, ya);
+          store8(yp + c.c1, yb);
         }
-        from_pairs(c, ya, yb);
-        T* dp = static_cast<T*>(a.dx[w].p) + a.dx[w].at(b, l, h);
-        store8(dp + c.c0, ya);
-        store8(dp + c.c1, yb);
+      } else {
+        float along = 0.f;
+        if (on) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float gya = ya[k] * cs[k] + yb[k] * sn[k];  // R^T dy
+            const float gyb = yb[k] * cs[k] - ya[k] * sn[k];
+            xa[k] *= r;
+            xb[k] *= r;
+            sum_a[k] = fmaf(gya, xa[k], sum_a[k]);
+            sum_b[k] = fmaf(gyb, xb[k], sum_b[k]);
+            ya[k] = gya * ga[k];
+            yb[k] = gyb * gb[k];
+            along = fmaf(ya[k], xa[k], fmaf(yb[k], xb[k], along));
+          }
+        }
+        along = group_sum<G>(along) * inv_d;
+        if (on) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            ya[k] = r * (ya[k] - xa[k] * along);
+            yb[k] = r * (yb[k] - xb[k] * along);
+          }
+          from_pairs<kInter>(ya, yb);
+          T* dp = static_cast<T*>(a.dx[w].p) + a.dx[w].at(b, l, h);
+          store8(dp + c.c0, ya);
+          store8(dp + c.c1, yb);
+        }
       }
     }
+    b += step_b;
+    l += step_l;
+    if (l >= a.L) l -= a.L, ++b;
   }
   if (kBackward) {
     // this block's share of dgamma: lanes of the same channels, then warps, in a fixed order
     __shared__ float s[kThreads / 32][kMaxD];
-    from_pairs(c, sum_a, sum_b);
+    from_pairs<kInter>(sum_a, sum_b);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
 #pragma unroll
@@ -260,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_vec_kernel(QkNormArgs a, int
         sum_a[k] += __shfl_xor_sync(0xffffffffu, sum_a[k], o);
         sum_b[k] += __shfl_xor_sync(0xffffffffu, sum_b[k], o);
       }
-      if (live && (threadIdx.x & 31) < G) {
+      if (t < a.d / 16 && (threadIdx.x & 31) < G) {
         s[threadIdx.x >> 5][c.c0 + k] = sum_a[k];
         s[threadIdx.x >> 5][c.c1 + k] = sum_b[k];
       }
@@ -370,21 +386,23 @@ __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(QkNormArgs a, int
   }
 }
 
-// dgamma = the blocks' shares added in a fixed order: 32 channels per block,
-// eight runs of blocks side by side.
-__global__ void __launch_bounds__(256) qk_norm_dgamma_kernel(QkNormArgs a, int qblocks, int blocks,
-                                                            const float* partial) {
-  __shared__ float s[8][33];
+// dgamma = the blocks' shares added in a fixed order: 32 channels per block, 32
+// runs of shares side by side.
+__global__ void __launch_bounds__(1024) qk_norm_dgamma_kernel(QkNormArgs a, int qblocks, int blocks,
+                                                             const float* partial) {
+  __shared__ float s[32][33];
   const int w = blockIdx.y, lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   const int lo = w ? qblocks : 0, hi = w ? blocks : qblocks;
   float v = 0.f;
-  if (c < a.d)
-    for (int b = lo + run; b < hi; b += 8) v += partial[(long long)b * a.d + c];
+  if (c < a.d) {
+#pragma unroll 4
+    for (int b = lo + run; b < hi; b += 32) v += partial[(long long)b * a.d + c];
+  }
   s[run][lane] = v;
   __syncthreads();
   if (run == 0 && c < a.d) {
-    for (int k = 1; k < 8; ++k) v += s[k][lane];
+    for (int k = 1; k < 32; ++k) v += s[k][lane];
     a.dgamma[w][c] = v;
   }
 }
@@ -411,12 +429,10 @@ int group_of(int d) {
   return g;
 }
 
-// Blocks of q and of k: enough rows in flight to fill the GPU (eight blocks of
-// 256 threads per SM), at most one step's rows per block when there are few.
-void grid_of(const QkNormArgs& a, int rows_per_block, int per_sm, int* q, int* k) {
+// Blocks of q and of k for steps of `need` rows or tokens: as many as are
+// resident, at most one step each when there are few.
+void grid_of(const QkNormArgs& a, const long long (&need)[2], int per_sm, int* q, int* k) {
   const long long cap = (long long)sm_count() * per_sm;
-  const long long need[2] = {((long long)a.B * a.L * a.heads[0] + rows_per_block - 1) / rows_per_block,
-                             ((long long)a.B * a.L * a.heads[1] + rows_per_block - 1) / rows_per_block};
   if (need[0] + need[1] <= cap) {
     *q = (int)need[0];
     *k = (int)need[1];
@@ -432,7 +448,27 @@ template <class T, bool kBackward>
 void plan(const QkNormArgs& a, bool* vec, int* G, int* nq, int* nk) {
   *vec = vec_ok(a, (int)sizeof(T), kBackward);
   *G = *vec ? group_of(a.d) : 32;
-  grid_of(a, kThreads / *G, kBackward ? 4 : 8, nq, nk);
+  long long need[2];
+  for (int w = 0; w < 2; ++w) {
+    const long long tokens = (long long)a.B * a.L;
+    const int groups = kThreads / *G, per = groups / a.heads[w] > 0 ? groups / a.heads[w] : 1;
+    need[w] = *vec ? (tokens + per - 1) / per : (tokens * a.heads[w] + groups - 1) / groups;
+  }
+  grid_of(a, need, kBackward ? 2 : 3, nq, nk);
+}
+
+template <class T, bool kBackward, bool kInter>
+void launch_vec(const QkNormArgs& a, int G, int grid, int nq, float* partial, cudaStream_t st) {
+  if (G == 1)
+    qk_norm_vec_kernel<T, 1, kBackward, kInter><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (G == 2)
+    qk_norm_vec_kernel<T, 2, kBackward, kInter><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (G == 4)
+    qk_norm_vec_kernel<T, 4, kBackward, kInter><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (G == 8)
+    qk_norm_vec_kernel<T, 8, kBackward, kInter><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else
+    qk_norm_vec_kernel<T, 16, kBackward, kInter><<<grid, kThreads, 0, st>>>(a, nq, partial);
 }
 
 template <class T, bool kBackward>
@@ -444,22 +480,16 @@ cudaError_t launch(const QkNormArgs& a, float* partial, cudaStream_t st) {
   prof_begin(kKindOther, st);
   if (!vec)
     qk_norm_any_kernel<T, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
-  else if (G == 1)
-    qk_norm_vec_kernel<T, 1, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
-  else if (G == 2)
-    qk_norm_vec_kernel<T, 2, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
-  else if (G == 4)
-    qk_norm_vec_kernel<T, 4, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
-  else if (G == 8)
-    qk_norm_vec_kernel<T, 8, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (a.interleaved && a.rot)
+    launch_vec<T, kBackward, true>(a, G, grid, nq, partial, st);
   else
-    qk_norm_vec_kernel<T, 16, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+    launch_vec<T, kBackward, false>(a, G, grid, nq, partial, st);
   prof_end(kKindOther, st);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !kBackward) return e;
   prof_begin(kKindOther, st);
-  qk_norm_dgamma_kernel<<<dim3((a.d + 31) / 32, 2), 256, 0, st>>>(a, nq, grid, partial);
+  qk_norm_dgamma_kernel<<<dim3((a.d + 31) / 32, 2), 1024, 0, st>>>(a, nq, grid, partial);
   prof_end(kKindOther, st);
   count_launch();
   return cudaGetLastError();

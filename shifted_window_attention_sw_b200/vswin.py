@@ -423,17 +423,24 @@ def wmsa_forward_host(x_host, window, shift, Wqkv, bqkv, Wproj, bproj, table, he
 
 
 # ------------------------------------------------------------------ token sequences
-def _heads(name, t, shape, dtype, device):
-    """View of a (B, L, heads, d) tensor; its channels have to be contiguous."""
+def _refuse(name, t, shape, dtype, device):
+    """Say what is wrong with a tensor that is not of this shape and type on this CUDA device."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous (its channels, if it has heads), got strides {t.stride()}")
+
+
+def _heads(name, t, shape, dtype, device):
+    """View of a (B, L, heads, d) tensor; its channels have to be contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        _refuse(name, t, shape, dtype, device)
     sb, st, sh, sd = t.stride()
     if sd != 1 and shape[3] > 1:
-        raise ValueError(f"{name} must have contiguous channels, got strides {t.stride()}")
+        _refuse(name, t, shape, dtype, device)
     return _Heads(t.data_ptr(), sb, st, sh)
 
 
@@ -441,15 +448,27 @@ def _flat(name, t, shape, dtype, device):
     """Pointer of a contiguous tensor of a given shape and type, None for None."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, device)
     return t.data_ptr()
+
+
+def _run(fn, dev, stream, *args):
+    """Calls an entry on a device's stream (its current one by default), with that device current."""
+    # (the raw forms of torch.cuda.current_stream and current_device: these calls take a few us in all)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != OK:
+        raise VswinError(status, last_error())
 
 
 def _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved):
@@ -459,6 +478,8 @@ def _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
         raise TypeError(f"q must be one of {list(DTYPES)}, got {q.dtype}")
     B, L, hq, d = q.shape
     hk, dt, dev = k.shape[2], q.dtype, q.device
+    if not q.is_cuda:
+        _refuse("q", q, q.shape, dt, dev)
     rot = None
     if cos is not None or sin is not None:
         if cos is None or sin is None or cos.dim() != 2:
@@ -482,11 +503,10 @@ def qk_norm_forward(q, k, gamma_q, gamma_k, eps=1e-6, cos=None, sin=None, positi
     them) of the float32 tables cos and sin, in one pass; bf16, fp16 or fp32. Views with contiguous channels
     are taken as they are. ``q_out`` may be ``q`` and ``k_out`` ``k``. Returns (q_out, k_out)."""
     (B, L, hq, hk, d, dt, dev), args = _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
-    q_out = torch.empty((B, L, hq, d), dtype=dt, device=dev) if q_out is None else q_out
-    k_out = torch.empty((B, L, hk, d), dtype=dt, device=dev) if k_out is None else k_out
-    with torch.cuda.device(dev):
-        _check(lib().vswin_qk_norm_forward(*args, _heads("q_out", q_out, (B, L, hq, d), dt, dev),
-                                           _heads("k_out", k_out, (B, L, hk, d), dt, dev), _stream_handle(stream, dev)))
+    q_out = q.new_empty((B, L, hq, d)) if q_out is None else q_out
+    k_out = q.new_empty((B, L, hk, d)) if k_out is None else k_out
+    _run(lib().vswin_qk_norm_forward, dev, stream, *args, _heads("q_out", q_out, (B, L, hq, d), dt, dev),
+         _heads("k_out", k_out, (B, L, hk, d), dt, dev))
     return q_out, k_out
 
 
@@ -495,14 +515,13 @@ def qk_norm_backward(q, k, gamma_q, gamma_k, dq_out, dk_out, eps=1e-6, cos=None,
     """Gradients (dq, dk in the type of q; dgamma_q, dgamma_k float32) of qk_norm_forward for the output
     gradients ``dq_out`` and ``dk_out``. ``dq`` and ``dk`` may be given, e.g. as slices of one buffer."""
     (B, L, hq, hk, d, dt, dev), args = _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
-    dq = torch.empty((B, L, hq, d), dtype=dt, device=dev) if dq is None else dq
-    dk = torch.empty((B, L, hk, d), dtype=dt, device=dev) if dk is None else dk
+    dq = q.new_empty((B, L, hq, d)) if dq is None else dq
+    dk = q.new_empty((B, L, hk, d)) if dk is None else dk
     dgamma = torch.empty((2, d), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().vswin_qk_norm_backward(
-            *args, _heads("dq_out", dq_out, (B, L, hq, d), dt, dev), _heads("dk_out", dk_out, (B, L, hk, d), dt, dev),
-            _heads("dq", dq, (B, L, hq, d), dt, dev), _heads("dk", dk, (B, L, hk, d), dt, dev),
-            dgamma[0].data_ptr(), dgamma[1].data_ptr(), _stream_handle(stream, dev)))
+    at = dgamma.data_ptr()
+    _run(lib().vswin_qk_norm_backward, dev, stream, *args, _heads("dq_out", dq_out, (B, L, hq, d), dt, dev),
+         _heads("dk_out", dk_out, (B, L, hk, d), dt, dev), _heads("dq", dq, (B, L, hq, d), dt, dev),
+         _heads("dk", dk, (B, L, hk, d), dt, dev), at, at + 4 * d)
     return dq, dk, dgamma[0], dgamma[1]
 
 
@@ -523,6 +542,8 @@ def _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens, kv_l
     B, Lq, hq, d = q.shape
     Lk, hk = k.shape[1:3]
     dt, dev = q.dtype, q.device
+    if not q.is_cuda:
+        _refuse("q", q, q.shape, dt, dev)
     if table.dim() != 2 or bucket_map.dim() != 1 or bucket_map.shape[0] % 2 == 0:
         raise ValueError("table must be (buckets, heads of q) and bucket_map (2 * max_distance + 1,), got "
                          f"{tuple(table.shape)} and {tuple(bucket_map.shape)}")
@@ -546,12 +567,10 @@ def bias_attention_forward(q, k, v, table, bucket_map, scale=None, causal=False,
     cache: Lq = 1, q_start = kv_lens - 1. Returns (out, lse), lse float32 (B, hq, Lq)."""
     (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
                                                                  kv_lens, q_start)
-    out = torch.empty((B, Lq, hq, d), dtype=dt, device=dev) if out is None else out
+    out = q.new_empty((B, Lq, hq, d)) if out is None else out
     lse = torch.empty((B, hq, Lq), dtype=torch.float32, device=dev) if lse is None else lse
-    with torch.cuda.device(dev):
-        _check(lib().vswin_bias_attention_forward(*args, _heads("out", out, (B, Lq, hq, d), dt, dev),
-                                                  _flat("lse", lse, (B, hq, Lq), torch.float32, dev),
-                                                  _stream_handle(stream, dev)))
+    _run(lib().vswin_bias_attention_forward, dev, stream, *args, _heads("out", out, (B, Lq, hq, d), dt, dev),
+         _flat("lse", lse, (B, hq, Lq), torch.float32, dev))
     return out, lse
 
 
@@ -562,13 +581,11 @@ def bias_attention_backward(q, k, v, table, bucket_map, out, lse, dout, scale=No
     (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
                                                                  kv_lens, q_start)
     qs, ks = (B, Lq, hq, d), (B, Lk, hk, d)
-    dq, dk, dv = (torch.empty(s, dtype=dt, device=dev) if t is None else t for t, s in ((dq, qs), (dk, ks), (dv, ks)))
+    dq, dk, dv = (q.new_empty(s) if t is None else t for t, s in ((dq, qs), (dk, ks), (dv, ks)))
     dtable = torch.empty_like(table)
-    with torch.cuda.device(dev):
-        _check(lib().vswin_bias_attention_backward(
-            *args, _heads("out", out, qs, dt, dev), _flat("lse", lse, (B, hq, Lq), torch.float32, dev),
-            _heads("dout", dout, qs, dt, dev), _heads("dq", dq, qs, dt, dev), _heads("dk", dk, ks, dt, dev),
-            _heads("dv", dv, ks, dt, dev), dtable.data_ptr(), _stream_handle(stream, dev)))
+    _run(lib().vswin_bias_attention_backward, dev, stream, *args, _heads("out", out, qs, dt, dev),
+         _flat("lse", lse, (B, hq, Lq), torch.float32, dev), _heads("dout", dout, qs, dt, dev),
+         _heads("dq", dq, qs, dt, dev), _heads("dk", dk, ks, dt, dev), _heads("dv", dv, ks, dt, dev), dtable.data_ptr())
     return dq, dk, dv, dtable
 
 
@@ -590,6 +607,8 @@ class AdamW:
             raise ValueError(f"bits must be 32 or 8, got {bits}")
         self.lr, self.betas, self.eps, self.bits, self.steps = lr, tuple(betas), eps, bits, 0
         dev = self.device = self.params[0].device
+        if not self.params[0].is_cuda:
+            _refuse("params[0]", self.params[0], self.params[0].shape, self.params[0].dtype, dev)
         decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(self.params)
         if len(decay) != len(self.params):
             raise ValueError(f"{len(decay)} weight decays for {len(self.params)} parameters")
@@ -641,8 +660,9 @@ class AdamW:
         captured step needs. grad_scale: one-element float32 CUDA tensor that multiplies every gradient."""
         grads = self._list("grads", grads)
         dev = self.device
+        types = DTYPES
         for i, (g, r, shape) in enumerate(zip(grads, self._records, self._shapes)):
-            dt = DTYPES.get(g.dtype)
+            dt = types.get(g.dtype)
             if dt is None or g.shape != shape or g.device != dev or not g.is_contiguous():
                 raise ValueError(f"grads[{i}] must be a contiguous {tuple(shape)} tensor of {list(DTYPES)} on {dev}, "
                                  f"got {g.dtype} {tuple(g.shape)} on {g.device}")
@@ -658,10 +678,8 @@ class AdamW:
         if grad_scale is not None and grad_scale.numel() != 1:
             raise ValueError("grad_scale must have one element")
         gs = None if grad_scale is None else _flat("grad_scale", grad_scale, tuple(grad_scale.shape), torch.float32, dev)
-        with torch.cuda.device(dev):
-            _check(lib().vswin_adamw_step(self._records, len(self._records), self.bits,
-                                          float(self.lr if lr is None else lr), *map(float, self.betas),
-                                          float(self.eps), count, count_dev, gs, _stream_handle(stream, dev)))
+        _run(lib().vswin_adamw_step, dev, stream, self._records, len(self._records), self.bits,
+             float(self.lr if lr is None else lr), *map(float, self.betas), float(self.eps), count, count_dev, gs)
         self.steps = count
         return self
 
@@ -677,15 +695,15 @@ class AdamW:
 def adamw_decode(m, m_scale, v, v_scale, dtype=torch.float32, stream=None):
     """(m, v) that 8-bit moments stand for: codes int8 and uint8 of one shape, scales float32 per 256 elements."""
     dev, shape = m.device, tuple(m.shape)
+    if not m.is_cuda:
+        _refuse("m", m, m.shape, m.dtype, dev)
     if dtype not in DTYPES:
         raise TypeError(f"dtype must be one of {list(DTYPES)}, got {dtype}")
     blocks = (-(-m.numel() // ADAMW_BLOCK),)
     args = (_flat("m", m, shape, torch.int8, dev), _flat("m_scale", m_scale, blocks, torch.float32, dev),
             _flat("v", v, shape, torch.uint8, dev), _flat("v_scale", v_scale, blocks, torch.float32, dev))
     mo, vo = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().vswin_adamw_decode(*args, m.numel(), DTYPES[dtype], mo.data_ptr(), vo.data_ptr(),
-                                        _stream_handle(stream, dev)))
+    _run(lib().vswin_adamw_decode, dev, stream, *args, m.numel(), DTYPES[dtype], mo.data_ptr(), vo.data_ptr())
     return mo, vo
 
 
