@@ -13,21 +13,26 @@
 // keys go by in tiles of 64: S = Q K^T on tcgen05 into one of two TMEM buffers
 // (fp32), four softmax warps (TMEM lane = query row) turn it into P (16 bits,
 // written over the scores, the A operand of a TS MMA) and O += P V accumulates
-// in TMEM. While the warps work on one tile, P V of the tile before and the
-// scores of the next run. Two producer warps bring K and V tiles (two or three
-// stages, TMA) and prepare each tile's bias; a tile in which the keys end goes
-// by cp.async instead, so that nothing behind the lengths is read.
+// in TMEM. D = 32 and 64: two groups of four warps take the tiles in turns, each
+// with its own buffer, softmax statistics and sums, joined at the end (sixteen
+// softmax warps per SM keep the exponentials busy while other warps wait for
+// their scores); D = 128, whose sums leave no room for a second set: one group,
+// and the scores of the next tile run while it works. One warp brings K and V
+// tiles (two or three stages, TMA; a tile in which the keys end goes by cp.async
+// instead, so that nothing behind the lengths is read), one prepares each tile's
+// bias.
 //
 // Bias: it depends on j - i alone, so a tile needs 127 + BN values, one line in
 // shared memory that row i reads from entry 127 - i on (consecutive rows,
 // consecutive banks); the causal rule is part of the line (-inf). Tiles of one
 // bucket (all far ones) skip the line: one value for the whole tile.
 //
-// Softmax in one pass: a tile's P is formed against the row's reference m, the
-// maximum as it was when it last moved, so that its exponentials do not wait
-// for its maximum. Only when a score exceeds m by more than kSlack (in log2)
-// does the warp raise m, form P again and rescale O; P is at most 2^kSlack, exact in fp32 sums and finite in 16 bits, and o and lse do not
-// depend on m. TMEM columns: scores [0, 64) and [64, 128), O behind.
+// Softmax in one pass over the keys, half a tile at a time: P is formed against
+// the row's reference m, the maximum as it was when it last moved. Only when a
+// score exceeds m by more than kSlack (in log2) does the warp raise m, by a whole
+// number, and rescale what it has by that power of two (without rounding); P is
+// at most 2^kSlack, exact in fp32 sums and finite in 16 bits, and o and lse do
+// not depend on m. TMEM columns: scores [0, 64) and [64, 128), O behind.
 //
 // Bound: one exponential per visible pair (16 per clock and SM) for D = 32 and
 // 64, the tensor cores for D = 128.
@@ -37,10 +42,7 @@
 namespace vswin {
 namespace {
 
-constexpr int kSoftmaxWarps = 4, kProducerWarps = 2;
-constexpr int kMmaWarp = 4;
-constexpr int kFwdThreads = 32 * (kSoftmaxWarps + 1 + kProducerWarps);
-constexpr int kProducers = 32 * kProducerWarps;
+constexpr int kProducerWarps = 2;
 constexpr float kSlack = 8.f;
 
 constexpr int kBn = 64;           // keys per tile
@@ -49,6 +51,9 @@ constexpr int kLineN = 127 + kBn;  // offsets in a tile
 
 template <int D>
 struct FwdCfg {
+  static constexpr int G = D == 128 ? 1 : 2;   // groups of four softmax warps, each with its own sums O
+  static constexpr int kMmaWarp = 4 * G;
+  static constexpr int THREADS = 32 * (4 * G + 1 + kProducerWarps);
   static constexpr int ST = D == 128 ? 2 : 3;  // stages: two CTAs share 227 KB
   using Line = BiasLine<kLineN, false>;
   static constexpr int kTile = kBn * D * 2;
@@ -57,10 +62,11 @@ struct FwdCfg {
   static constexpr int OFF_V = OFF_K + ST * kTile;
   static constexpr int OFF_BIAS = OFF_V + ST * kTile;
   static constexpr int OFF_BAR = OFF_BIAS + (ST * (int)sizeof(Line) + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_BAR + 256;
+  static constexpr int OFF_ML = OFF_BAR + 256;  // [G][128] (m, l) of the groups' rows
+  static constexpr int SMEM = OFF_ML + (G == 2 ? 2 * 128 * 8 : 0);
   static constexpr int kColO = 2 * kBn;
   static constexpr uint32_t kTmem = 256;
-  static_assert(kColO + D <= 256, "TMEM columns of a CTA");
+  static_assert(kColO + G * D <= 256, "TMEM columns of a CTA");
 };
 
 struct FwdParams {
@@ -69,11 +75,11 @@ struct FwdParams {
 };
 
 template <class T, int D>
-__global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_constant__ FwdParams params, Split sp) {
+__global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const __grid_constant__ FwdParams params, Split sp) {
   const BiasAttnArgs& a = params.a;
   using C = FwdCfg<D>;
   using Line = typename C::Line;
-  constexpr int ST = C::ST;
+  constexpr int ST = C::ST, G = C::G, kMmaWarp = C::kMmaWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   Line* lines = reinterpret_cast<Line*>(smem + C::OFF_BIAS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -83,9 +89,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
   uint64_t* v_free = bars + 3 * ST;   // [ST]
   uint64_t* s_full = bars + 4 * ST;   // [ST] bias line written and scores in TMEM
   uint64_t* p_full = bars + 5 * ST;   // [2] P written over them
-  uint64_t* o_done = p_full + 2;      // P V accumulated
-  uint64_t* q_full = p_full + 3;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(p_full + 4);
+  uint64_t* o_done = p_full + 2;      // [2] P V accumulated
+  uint64_t* q_full = p_full + 4;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(p_full + 5);
+  float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // heavy query tiles (causal: the last) first
@@ -106,15 +113,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
 
   if (tid == 0) {
     for (int k = 0; k < ST; ++k) {
-      mbar_init(&k_full[k], kProducerWarps);
+      mbar_init(&k_full[k], 1);
       mbar_init(&k_free[k], 1);
-      mbar_init(&v_full[k], kProducerWarps);
+      mbar_init(&v_full[k], 1);
       mbar_init(&v_free[k], 1);
-      mbar_init(&s_full[k], kProducerWarps + 1);
+      mbar_init(&s_full[k], 2);
     }
-    for (int k = 0; k < 2; ++k) mbar_init(&p_full[k], kSoftmaxWarps);
-    mbar_init(o_done, 1);
-    mbar_init(q_full, kProducerWarps);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&p_full[k], 4);
+      mbar_init(&o_done[k], 1);
+    }
+    mbar_init(q_full, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -127,21 +136,28 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
   const uint32_t tmem = *s_tmem;
 
   if (warp > kMmaWarp) {
-    // ------------------------------------------------------------ producers
-    const int p = tid - 32 * (kMmaWarp + 1);
+    // ------------------------------------------------------------ producers: tiles, bias lines
     const uint32_t sq = smem_u32(smem + C::OFF_Q), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
-    if (nt > 0) bring_tile<T, D, 128>(sq, params.q, a.q, b, h, i0, sl.nq, a.Lq, q_full, p);
     int s = 0;
     uint32_t parity = 1;  // of the stage's previous use
-    for (int t = 0; t < nt; ++t) {
-      const int j0 = (t0 + t) * kBn;
-      if (t >= ST && !warp_wait(&k_free[s], parity, a.ctx, kErrAttnLoad)) break;
-      bring_tile<T, D, kBn>(sk + s * C::kTile, params.k, a.k, b, hk, j0, sl.nk, a.Lk, &k_full[s], p);
-      if (t >= ST && !warp_wait(&v_free[s], parity, a.ctx, kErrAttnLoad)) break;
-      bring_tile<T, D, kBn>(sv + s * C::kTile, params.v, a.v, b, hk, j0, sl.nk, a.Lk, &v_full[s], p);
-      fill_bias_line<T, kLineN, false, kProducers>(&lines[s], a, h, j0 - pos0 - 127, p);
-      if (lane == 0) mbar_arrive(&s_full[s]);  // (the line was free when V was)
-      if (++s == ST) s = 0, parity ^= 1;
+    if (warp == kMmaWarp + 1) {
+      if (nt > 0) bring_tile<T, D, 128>(sq, params.q, a.q, b, h, i0, sl.nq, a.Lq, q_full);
+      for (int t = 0; t < nt; ++t) {
+        const int j0 = (t0 + t) * kBn;
+        if (t >= ST && !warp_wait(&k_free[s], parity, a.ctx, kErrAttnLoad)) break;
+        bring_tile<T, D, kBn>(sk + s * C::kTile, params.k, a.k, b, hk, j0, sl.nk, a.Lk, &k_full[s]);
+        if (t >= ST && !warp_wait(&v_free[s], parity, a.ctx, kErrAttnLoad)) break;
+        bring_tile<T, D, kBn>(sv + s * C::kTile, params.v, a.v, b, hk, j0, sl.nk, a.Lk, &v_full[s]);
+        if (++s == ST) s = 0, parity ^= 1;
+      }
+    } else if (nt > 0) {
+      const LineWriter<T, kLineN, false> writer(a, h);
+      for (int t = 0; t < nt; ++t) {
+        if (t >= ST && !warp_wait(&v_free[s], parity, a.ctx, kErrAttnLoad)) break;  // (P V follows every read of the line)
+        writer.write(&lines[s], (t0 + t) * kBn - pos0 - 127);
+        if (lane == 0) mbar_arrive(&s_full[s]);
+        if (++s == ST) s = 0, parity ^= 1;
+      }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
@@ -169,8 +185,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_acc<D, kBn>(tmem + C::kColO, tmem + kBn * (t & 1), sv + vs * C::kTile, id_o, t == 0);
-        umma_commit(o_done);
+        mma_acc<D, kBn>(tmem + C::kColO + (G == 2 ? (t & 1) * D : 0), tmem + kBn * (t & 1), sv + vs * C::kTile, id_o, t < G);
+        umma_commit(&o_done[t & 1]);
         umma_commit(&v_free[vs]);
       }
       __syncwarp();
@@ -179,140 +195,164 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const uint32_t tw = tmem + ((uint32_t)(warp * 32) << 16);
-    const int i = i0 + warp * 32 + lane;
+    const int g = warp >> 2, row = (warp & 3) * 32 + lane, i = i0 + row;
+    const uint32_t tw = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to = tw + C::kColO + g * D;
     const float c = a.scale * kLog2E;
     const float2 c2 = make_float2(c, c);
     float m = 0.f;  // reference of the row (log2), once l > 0
     float l = 0.f;  // sum of P
     bool ok = true;
-    int s = 0;
+    int s = g;
     uint32_t parity = 0;
-    for (int t = 0; t < nt; ++t) {
+    for (int t = g; t < nt; t += G) {
       ok = warp_wait(&s_full[s], parity, a.ctx, kErrAttnSoftmax);
       if (!ok) break;
       tc_fence_after();
       const uint32_t buf = tw + kBn * (t & 1);
-      uint32_t u[kBn];
-      tmem_ld32(buf, u);
-      tmem_ld32(buf + 32, u + 32);
       const Line& bl = lines[s];
-      const bool flat = bl.same[0] && bl.same[1];
+      const bool flat = bl.flat != 0;
       const float value = bl.value;
-      const float* line = bl.line + 127 - (warp * 32 + lane);
+      const float* line = bl.line + 127 - row;
       const int live = nk - (t0 + t) * kBn;  // columns of the tile that are keys
-      tmem_wait_ld_keep(u);
-      float x[kBn];  // S c + bias - m
-      if (flat) {
-        const float2 off = make_float2(value - m, value - m);
+      uint32_t w[16];                        // P of the first half
+      // one half of the tile: of one bucket or not, with keys missing or not
+      auto half = [&](auto second_, auto flat_, auto cut_) {
+        constexpr int c0 = decltype(second_)::value ? 32 : 0;
+        constexpr bool kFlat = decltype(flat_)::value, kCut = decltype(cut_)::value;
+        uint32_t u[32];
+        tmem_ld32(buf + c0, u);
+        tmem_wait_ld_keep(u);
+        float x[32];  // S c + bias - m
+        const float off = kFlat ? value - m : -m;
 #pragma unroll
-        for (int k = 0; k < kBn; k += 2) {
-          const float2 y = __ffma2_rn(make_float2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), c2, off);
-          x[k] = y.x;
-          x[k + 1] = y.y;
+        for (int k = 0; k < 32; k += 2) {
+          float2 y = make_float2(off, off);
+          if (!kFlat) y = __fadd2_rn(make_float2(line[c0 + k], line[c0 + k + 1]), y);
+          y = __ffma2_rn(make_float2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), c2, y);
+          x[k] = !kCut || c0 + k < live ? y.x : -INFINITY;
+          x[k + 1] = !kCut || c0 + k + 1 < live ? y.y : -INFINITY;
         }
-      } else {
-        const float2 mm = make_float2(-m, -m);
+        float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < kBn; k += 2) {
-          const float2 off = __fadd2_rn(make_float2(line[k], line[k + 1]), mm);
-          const float2 y = __ffma2_rn(make_float2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), c2, off);
-          x[k] = y.x;
-          x[k + 1] = y.y;
-        }
-      }
-      if (live < kBn) {
+        for (int k = 0; k < 32; k += 2) tops[k / 2 % 2] = max3(tops[k / 2 % 2], x[k], x[k + 1]);
+        const float top = fmaxf(tops[0], tops[1]);
+        const bool move = l == 0.f ? top > -INFINITY : top > kSlack;
+        if (__any_sync(0xffffffffu, move)) {
+          // by whole powers of two, so that what is there already is rescaled without rounding
+          const float step = move ? ceilf(top) : 0.f;
+          const float alpha = step < 127.f ? __int_as_float((127 - max((int)step, 0)) << 23) : 0.f;
+          m += step;
+          l *= alpha;
 #pragma unroll
-        for (int k = 0; k < kBn; ++k) x[k] = k < live ? x[k] : -INFINITY;
-      }
-      // P against the reference as it stands, while the maximum is found beside it
-      uint32_t w[kBn / 2];
-      float2 acc;
-      auto form = [&]() {
-        acc = make_float2(0.f, 0.f);
+          for (int k = 0; k < 32; ++k) x[k] -= step;
+          if (c0) {
+            const uint32_t a2 = pack2<T>(alpha, alpha);
 #pragma unroll
-        for (int k = 0; k < kBn; k += 2) {
-          const float2 p = make_float2(ex2(x[k]), ex2(x[k + 1]));
-          acc = __fadd2_rn(acc, p);
-          w[k / 2] = pack2<T>(p.x, p.y);
-        }
-      };
-      form();
-      float tops[4] = {x[0], x[1], x[2], x[3]};
+            for (int k = 0; k < 16; ++k) w[k] = mul2<T>(w[k], a2);
+          }
+          if (t >= G) {  // (the group's sums so far: complete before these scores were, or waited for)
+            if (G == 1 && !warp_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, a.ctx, kErrAttnSoftmax)) return false;
+            tc_fence_after();
 #pragma unroll
-      for (int k = 4; k < kBn; k += 8) {
+            for (int e = 0; e < D; e += 8) {
+              uint32_t r[8];
+              tmem_ld8(to + e, r);
+              tmem_wait_ld_keep(r);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) tops[e] = k + 4 + e < kBn ? max3(tops[e], x[k + e], x[k + 4 + e]) : fmaxf(tops[e], x[k + e]);
-      }
-      const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-      const bool move = l == 0.f ? top > -INFINITY : top > kSlack;
-      if (__any_sync(0xffffffffu, move)) {
-        const float alpha = move ? (l == 0.f ? 0.f : ex2(-top)) : 1.f;
-        const float shift = move ? top : 0.f;
-        m += shift;
-        l *= alpha;
-#pragma unroll
-        for (int k = 0; k < kBn; ++k) x[k] -= shift;
-        form();
-        if (t > 0) {
-          ok = warp_wait(o_done, (t - 1) & 1, a.ctx, kErrAttnSoftmax);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t r[16];
-            tmem_ld16(tw + C::kColO + c0, r);
-            tmem_wait_ld_keep(r);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
-            tmem_st16(tw + C::kColO + c0, r);
+              for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
+              tmem_st8(to + e, r);
+            }
           }
         }
-      }
-      tmem_st16(buf, w);
-      tmem_st16(buf + 16, w + 16);
-      l += acc.x + acc.y;
+        if (c0) tmem_st16(buf, w);  // (every score of the tile is in registers)
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 32; e += 16) {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const float2 p = make_float2(ex2(x[e + k]), ex2(x[e + k + 1]));
+            acc = __fadd2_rn(acc, p);
+            (c0 ? v[k / 2] : w[e / 2 + k / 2]) = pack2<T>(p.x, p.y);
+          }
+          if (c0) tmem_st8(buf + 16 + e / 2, v);
+        }
+        l += acc.x + acc.y;
+        return true;
+      };
+      using Yes = std::true_type;
+      using No = std::false_type;
+      if (live >= kBn)
+        ok = flat ? half(No{}, Yes{}, No{}) && half(Yes{}, Yes{}, No{}) : half(No{}, No{}, No{}) && half(Yes{}, No{}, No{});
+      else
+        ok = flat ? half(No{}, Yes{}, Yes{}) && half(Yes{}, Yes{}, Yes{}) : half(No{}, No{}, Yes{}) && half(Yes{}, No{}, Yes{});
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[t & 1]);
-      if (++s == ST) s = 0, parity ^= 1;
+      s += G;
+      if (s >= ST) s -= ST, parity ^= 1;
     }
-    if (ok && nt > 0) ok = warp_wait(o_done, (nt - 1) & 1, a.ctx, kErrAttnSoftmax);
+    const int last = nt - 1 - (G == 2 ? (nt - 1 - g) & 1 : 0);  // the group's last tile
+    if (ok && last >= 0) ok = warp_wait(&o_done[last & 1], (last >> 1) & 1, a.ctx, kErrAttnSoftmax);
     tc_fence_after();
+    // the groups' sums over their tiles of the row, weighed against the larger reference; a group without any has weight 0
+    float weight[2] = {1.f, 0.f};
+    if (G == 2) {
+      ml[g * 128 + row] = make_float2(m, l);
+      tc_fence_before();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      tc_fence_after();
+      const float2 x = ml[row], y = ml[128 + row];
+      m = y.y == 0.f ? x.x : (x.y == 0.f ? y.x : fmaxf(x.x, y.x));
+      weight[0] = x.y == 0.f ? 0.f : ex2(x.x - m);
+      weight[1] = y.y == 0.f ? 0.f : ex2(y.x - m);
+      l = (x.y == 0.f ? 0.f : x.y * weight[0]) + (y.y == 0.f ? 0.f : y.y * weight[1]);
+    }
     if (ok) {
-      const bool row = i < a.Lq;
+      const bool in = i < a.Lq;
       const bool some = i < sl.nq && (l > 0.f || l != l);
       const float inv = some ? 1.f / l : 0.f;
       const long long r = ((long long)b * a.hq + h) * a.Lq + i;
-      if (row) {
+      if (in && g == 0) {
         if (sp.n == 1)
           a.lse[r] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
         else
           sp.lse[(long long)split * a.B * a.hq * a.Lq + r] = some ? m + log2f(l) : -INFINITY;
       }
-      T* out = static_cast<T*>(a.o.p) + (row ? a.o.at(b, i, h) : 0);
-      float* part = sp.o + ((long long)split * a.B * a.hq * a.Lq + (row ? r : 0)) * D;
+      T* out = static_cast<T*>(a.o.p) + (in ? a.o.at(b, i, h) : 0);
+      float* part = sp.o + ((long long)split * a.B * a.hq * a.Lq + (in ? r : 0)) * D;
+      // each group writes its part of the channels
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 16) {
-        uint32_t u[16];
-        if (nt > 0) {
-          tmem_ld16(tw + C::kColO + c0, u);
-          tmem_wait_ld_keep(u);
-        }
+      for (int c0 = 0; c0 < D / G; c0 += 16) {
+        const int ch = g * (D / G) + c0;
         float f[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) f[k] = some ? __uint_as_float(u[k]) * inv : 0.f;
-        if (row && sp.n == 1) {
+        for (int k = 0; k < 16; ++k) f[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          uint32_t u[16];
+          if (nt > e) {
+            tmem_ld16(tw + C::kColO + e * D + ch, u);
+            tmem_wait_ld_keep(u);
+          }
+          // (a sum of weight 0 may be anything, a NaN row has l NaN)
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (some && weight[e] != 0.f) f[k] = fmaf(__uint_as_float(u[k]), weight[e] * inv, f[k]);
+        }
+        if (in && sp.n == 1) {
 #pragma unroll
           for (int k = 0; k < 16; k += 8)
-            *reinterpret_cast<uint4*>(out + c0 + k) =
+            *reinterpret_cast<uint4*>(out + ch + k) =
                 make_uint4(pack2<T>(f[k], f[k + 1]), pack2<T>(f[k + 2], f[k + 3]), pack2<T>(f[k + 4], f[k + 5]),
                            pack2<T>(f[k + 6], f[k + 7]));
-        } else if (row) {
+        } else if (in) {
 #pragma unroll
           for (int k = 0; k < 16; k += 4)
-            *reinterpret_cast<float4*>(part + c0 + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+            *reinterpret_cast<float4*>(part + ch + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
         }
       }
     }
@@ -350,7 +390,7 @@ cudaError_t forward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
   make_head_map(&params.v, a.v, a.B, a.Lk, a.hk, D, dtype, kBn);
   const long long grid = (long long)a.B * a.hq * ((a.Lq + 127) / 128) * sp.n;
   prof_begin(kKindOther, st);
-  attn_fwd_kernel<T, D><<<(unsigned)grid, kFwdThreads, C::SMEM, st>>>(params, sp);
+  attn_fwd_kernel<T, D><<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(params, sp);
   prof_end(kKindOther, st);
   count_launch();
   e = cudaGetLastError();

@@ -76,6 +76,12 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <>
@@ -87,6 +93,18 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <class T>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v =
+        __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 }
 
 // Instruction descriptor of an MMA on T (both operands) with fp32 accumulation.
@@ -172,17 +190,17 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const T* head, long long
   }
 }
 
-// Rows [r0, r0 + ROWS) of head h of sequence b into a tile, by two producer
-// warps (p: thread of the 64), whose leaders' arrivals complete `bar` (count 2)
-// with the copies. n of the L rows take part: whole tiles go by TMA (which
-// reads zeros behind L); a tile in which the length ends goes by cp.async,
-// which reads nothing behind it, whatever it holds.
+// Rows [r0, r0 + ROWS) of head h of sequence b into a tile, by one warp, whose
+// one arrival completes `bar` with the copies. n of the L rows take part: whole
+// tiles go by TMA (which reads zeros behind L); a tile in which the length ends
+// goes by cp.async, which reads nothing behind it, whatever it holds.
 template <class T, int D, int ROWS>
 __device__ __forceinline__ void bring_tile(uint32_t dst, const HeadMap& m, const Heads& v, int b, int h, int r0, int n,
-                                           int L, uint64_t* bar, int p) {
+                                           int L, uint64_t* bar) {
   using Tl = TileOf<D>;
+  const int lane = threadIdx.x & 31;
   if (m.use && (r0 + ROWS <= n || n == L)) {
-    if (p == 0) {
+    if (lane == 0) {
       mbar_arrive_expect_tx(bar, ROWS * D * 2);
 #pragma unroll
       for (int c = 0; c < D; c += Tl::kPiece)
@@ -191,15 +209,13 @@ __device__ __forceinline__ void bring_tile(uint32_t dst, const HeadMap& m, const
             "%5}], [%6];" ::"r"(dst + c / Tl::kPiece * ROWS * Tl::kRow),
             "l"(reinterpret_cast<uint64_t>(&m.map)), "r"(c), "r"(r0), "r"(h * m.hmul), "r"(b * m.bmul), "r"(smem_u32(bar))
             : "memory");
-    } else if (p == 32) {
-      mbar_arrive(bar);
     }
   } else {
-    load_tile<T, D, ROWS, 64>(dst, static_cast<const T*>(v.p) + v.at(b, 0, h), v.st, r0, n, p);
+    load_tile<T, D, ROWS, 32>(dst, static_cast<const T*>(v.p) + v.at(b, 0, h), v.st, r0, n, lane);
     cp_async_wait_all();
     fence_proxy_async_smem();  // bytes written by cp.async are read by the tensor core
     __syncwarp();
-    if ((p & 31) == 0) mbar_arrive(bar);
+    if (lane == 0) mbar_arrive(bar);
   }
 }
 
@@ -223,50 +239,72 @@ __device__ __forceinline__ bool elect_one() {
 // The bias of a 128 x BN tile depends on the offset of key and query alone, so
 // it is one line of N = 127 + BN values, entry t at offset base + t: row i and
 // column j read entry j - i + 127 (rows are queries) or i - j + BN - 1 (rows are
-// keys). Written by whole warps; `same` of each warp says whether all its
-// entries equal entry 0, `value` and `which` (far tiles have one bucket: their
-// rows read no line at all). With kBuckets the buckets are kept too, and
-// entries are the same only if their buckets are.
+// keys). A line whose entries are all the same (`flat`; far tiles have one
+// bucket) is only `value` and its bucket `which`. With kBuckets the buckets are
+// kept too, and entries are the same only if their buckets are.
 template <int N, bool kBuckets>
 struct BiasLine {
   float line[N + 1];
   uint16_t bucket[kBuckets ? N + 1 : 2];
   float value;
   int which;
-  int same[2];
+  int flat;
 };
-template <class T, int N, bool kBuckets, int THREADS>
-__device__ __forceinline__ void fill_bias_line(BiasLine<N, kBuckets>* o, const BiasAttnArgs& a, int h, int base, int p) {
-  static_assert(THREADS == 64, "two warps");
-  int which = 0;
-  auto entry = [&](int rel, int* k) {
+
+// One warp writes lines of a head: the values beyond the map's ends are held, so
+// that far tiles read nothing.
+template <class T, int N, bool kBuckets>
+struct LineWriter {
+  const BiasAttnArgs& a;
+  int h, low_which, high_which;
+  float low, high;
+
+  __device__ __forceinline__ float entry(int rel, int* k) const {
     const float v = bias_of<T>(a, rel, h, k) * kLog2E;
     return a.causal && rel > 0 ? -INFINITY : v;  // the causal rule is part of the line
-  };
-  const float first = entry(base, &which);
-  bool same = true;
-  // a tile beyond one of the map's ends, on one side of the causal border
-  const bool far = base > a.D || base + N - 1 <= -a.D;
-  if (!far) {
+  }
+  __device__ __forceinline__ LineWriter(const BiasAttnArgs& args, int head) : a(args), h(head) {
+    low = entry(-a.D, &low_which);
+    high = entry(a.D + 1, &high_which);
+  }
+  __device__ __forceinline__ void head(int head) {
+    if (head == h) return;
+    h = head;
+    low = entry(-a.D, &low_which);
+    high = entry(a.D + 1, &high_which);
+  }
+  __device__ __forceinline__ void write(BiasLine<N, kBuckets>* o, int base) const {
+    const int lane = threadIdx.x & 31;
+    // a tile beyond one of the map's ends, on one side of the causal border
+    bool flat = base > a.D || base + N - 1 <= -a.D;
+    float value = base > a.D ? high : low;
+    int which = base > a.D ? high_which : low_which;
+    if (!flat) {
+      float v[(N + 31) / 32];
+      int k[(N + 31) / 32];
 #pragma unroll
-    for (int t = 0; t < N; t += THREADS) {
-      if (t + p < N) {
-        int k = 0;
-        const float v = entry(base + t + p, &k);
-        o->line[t + p] = v;
-        if (kBuckets) o->bucket[t + p] = (uint16_t)k;
-        same = same && v == first && (!kBuckets || k == which);
+      for (int t = 0; t < (N + 31) / 32; ++t) v[t] = entry(base + min(32 * t + lane, N - 1), &k[t]);
+      value = __shfl_sync(0xffffffffu, v[0], 0);
+      which = __shfl_sync(0xffffffffu, k[0], 0);
+      flat = true;
+#pragma unroll
+      for (int t = 0; t < (N + 31) / 32; ++t) {
+        if (32 * t + lane < N) {
+          o->line[32 * t + lane] = v[t];
+          if (kBuckets) o->bucket[32 * t + lane] = (uint16_t)k[t];
+        }
+        flat = flat && v[t] == value && (!kBuckets || k[t] == which);
       }
+      flat = __all_sync(0xffffffffu, flat);
     }
+    if (lane == 0) {
+      o->value = value;
+      o->which = which;
+      o->flat = flat;
+    }
+    __syncwarp();  // the leader's arrival stands for the warp
   }
-  same = __all_sync(0xffffffffu, same);
-  if ((p & 31) == 0) o->same[p >> 5] = same;
-  if (p == 0) {
-    o->value = first;
-    o->which = which;
-  }
-  __syncwarp();  // a leader's arrival stands for its warp
-}
+};
 
 // Map of a tensor of B x L x H rows of d channels in boxes of `rows` rows; false
 // (m->use = 0) when its strides have no map.

@@ -30,7 +30,6 @@ namespace {
 
 constexpr int kBn = 64;             // moving rows per tile
 constexpr int kLineN = 127 + kBn;   // offsets in a tile
-constexpr int kProducers = 64;
 
 template <int D, bool kKeys>
 struct BwdCfg {
@@ -103,14 +102,14 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
 
   if (tid == 0) {
     for (int k = 0; k < ST; ++k) {
-      mbar_init(&full[k], 3 * 2);
+      mbar_init(&full[k], 3);
       mbar_init(&free_[k], 1 + 4);
     }
     for (int k = 0; k < G; ++k) {
       mbar_init(&s_full[k], 1);
       mbar_init(&ds_full[k], 4);
     }
-    mbar_init(f_full, 2 * 2);
+    mbar_init(f_full, 2);
     mbar_init(done, 1);
     fence_mbar_init();
   }
@@ -125,39 +124,53 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
   const uint32_t sf = smem_u32(smem + C::OFF_F), sm = smem_u32(smem + C::OFF_M);
 
   if (warp > kMmaWarp) {
-    // ------------------------------------------------------------ producers
-    const int p = tid - 32 * (kMmaWarp + 1);
-    const Heads &F1 = kKeys ? a.k : a.q, &F2 = kKeys ? a.v : a.dout, &M1 = kKeys ? a.q : a.k, &M2 = kKeys ? a.dout : a.v;
-    const int fn = kKeys ? sl.nk : sl.nq, fL = kKeys ? a.Lk : a.Lq;
-    const int mn = kKeys ? sl.nq : sl.nk, mL = kKeys ? a.Lq : a.Lk;
-    if (nt > 0) {
-      bring_tile<T, D, 128>(sf, args.f1, F1, b, hf, f0, fn, fL, f_full, p);
-      bring_tile<T, D, 128>(sf + C::kFixed, args.f2, F2, b, hf, f0, fn, fL, f_full, p);
-    }
+    // ------------------------------------------------------------ producers: tiles; bias lines and columns
     int s = 0, u = 0, r0 = m_lo, h = kKeys ? hk * group : hf;
     uint32_t parity = 1;  // of the stage's previous use
-    for (int t = 0; t < nt; ++t) {
-      if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad)) break;
-      const int hm = kKeys ? h : hk;
-      const uint32_t dst = sm + s * 2 * C::kMoving;
-      bring_tile<T, D, kBn>(dst, args.m1, M1, b, hm, r0, mn, mL, &full[s], p);
-      bring_tile<T, D, kBn>(dst + C::kMoving, args.m2, M2, b, hm, r0, mn, mL, &full[s], p);
-      if constexpr (kKeys) {
-        float2 c = make_float2(-INFINITY, 0.f);  // a query that takes no part: P = 0
-        if (r0 + p < m_hi) {
-          const long long r = ((long long)b * a.hq + h) * a.Lq + r0 + p;
-          const float lse = a.lse[r];
-          if (lse != -INFINITY) c = make_float2(-lse * kLog2E, -args.delta[r]);
-        }
-        cols[s * kBn + p] = c;  // (fill_bias_line syncs the warp)
-        fill_bias_line<T, kLineN, false, kProducers>(&lines[s], a, h, f0 - (sl.start + r0) - (kBn - 1), p);
-      } else {
-        fill_bias_line<T, kLineN, true, kProducers>(&lines[s], a, h, r0 - (sl.start + f0) - 127, p);
+    if (warp == kMmaWarp + 1) {
+      const Heads &F1 = kKeys ? a.k : a.q, &F2 = kKeys ? a.v : a.dout, &M1 = kKeys ? a.q : a.k, &M2 = kKeys ? a.dout : a.v;
+      const int fn = kKeys ? sl.nk : sl.nq, fL = kKeys ? a.Lk : a.Lq;
+      const int mn = kKeys ? sl.nq : sl.nk, mL = kKeys ? a.Lq : a.Lk;
+      if (nt > 0) {
+        bring_tile<T, D, 128>(sf, args.f1, F1, b, hf, f0, fn, fL, f_full);
+        bring_tile<T, D, 128>(sf + C::kFixed, args.f2, F2, b, hf, f0, fn, fL, f_full);
       }
-      if (lane == 0) mbar_arrive(&full[s]);
-      if (++s == ST) s = 0, parity ^= 1;
-      r0 += kBn;
-      if (++u == per_head) u = 0, r0 = m_lo, ++h;
+      for (int t = 0; t < nt; ++t) {
+        if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad)) break;
+        const int hm = kKeys ? h : hk;
+        const uint32_t dst = sm + s * 2 * C::kMoving;
+        bring_tile<T, D, kBn>(dst, args.m1, M1, b, hm, r0, mn, mL, &full[s]);
+        bring_tile<T, D, kBn>(dst + C::kMoving, args.m2, M2, b, hm, r0, mn, mL, &full[s]);
+        if (++s == ST) s = 0, parity ^= 1;
+        r0 += kBn;
+        if (++u == per_head) u = 0, r0 = m_lo, ++h;
+      }
+    } else if (nt > 0) {
+      LineWriter<T, kLineN, !kKeys> writer(a, h);
+      for (int t = 0; t < nt; ++t) {
+        if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad)) break;
+        if constexpr (kKeys) {
+#pragma unroll
+          for (int e = 0; e < kBn; e += 32) {
+            const int i = r0 + e + lane;
+            float2 c = make_float2(-INFINITY, 0.f);  // a query that takes no part: P = 0
+            if (i < m_hi) {
+              const long long r = ((long long)b * a.hq + h) * a.Lq + i;
+              const float lse = a.lse[r];
+              if (lse != -INFINITY) c = make_float2(-lse * kLog2E, -args.delta[r]);
+            }
+            cols[s * kBn + e + lane] = c;
+          }
+          writer.head(h);
+          writer.write(&lines[s], f0 - (sl.start + r0) - (kBn - 1));
+        } else {
+          writer.write(&lines[s], r0 - (sl.start + f0) - 127);
+        }
+        if (lane == 0) mbar_arrive(&full[s]);
+        if (++s == ST) s = 0, parity ^= 1;
+        r0 += kBn;
+        if (++u == per_head) u = 0, r0 = m_lo, ++h;
+      }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
       if (!ok) break;
       tc_fence_after();
       const Line& bl = lines[s];
-      const bool flat = bl.same[0] && bl.same[1];
+      const bool flat = bl.flat != 0;
       const float value = bl.value;
       const float* line = bl.line + (kKeys ? kBn - 1 + row : 127 - row);
       const float2* col = cols + s * kBn;
