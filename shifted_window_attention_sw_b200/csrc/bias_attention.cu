@@ -27,7 +27,7 @@
 // consecutive banks); the causal rule is part of the line (-inf). Tiles of one
 // bucket (all far ones) skip the line: one value for the whole tile.
 //
-// Softmax in one pass over the keys, half a tile at a time: P is formed against
+// Softmax in one pass over the keys (half a tile at a time with two groups): P is formed against
 // the row's reference m, the maximum as it was when it last moved. Only when a
 // score exceeds m by more than kSlack (in log2) does the warp raise m, by a whole
 // number, and rescale what it has by that power of two (without rounding); P is
@@ -166,32 +166,46 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     constexpr uint32_t id_s = idesc16<T>(128, kBn, 0, 0), id_o = idesc16<T>(128, D, 0, 1);
     int ks = 0, vs = 0;
     uint32_t kp = 0, vp = 0;
-    auto scores = [&](int t) {
-      if (!warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_rows<D, kBn>(tmem + kBn * (t & 1), sq, sk + ks * C::kTile, id_s);
-        umma_commit(&s_full[ks]);
-        umma_commit(&k_free[ks]);
-      }
-      __syncwarp();
+    auto scores = [&](int t) {  // by the elected lane
+      mma_rows<D, kBn>(tmem + kBn * (t & 1), sq, sk + ks * C::kTile, id_s);
+      umma_commit(&s_full[ks]);
+      umma_commit(&k_free[ks]);
+    };
+    auto next_k = [&]() {
       if (++ks == ST) ks = 0, kp ^= 1;
-      return true;
     };
     bool ok = nt > 0 && warp_wait(q_full, 0, a.ctx, kErrAttnMma);
-    for (int t = 0; t < 2 && t < nt && ok; ++t) ok = scores(t);
+    for (int t = 0; t < 2 && t < nt && ok; ++t) {
+      ok = warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) scores(t);
+      __syncwarp();
+      next_k();
+    }
     for (int t = 0; t < nt && ok; ++t) {
+      const bool more = t + 2 < nt;
       ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t & 1], (t >> 1) & 1, a.ctx, kErrAttnMma);
       if (!ok) break;
+      // the scores that follow go out at once when their keys are there
+      const bool now = more && __all_sync(0xffffffffu, mbar_test(&k_full[ks], kp));
       tc_fence_after();
       if (elect_one()) {
         mma_acc<D, kBn>(tmem + C::kColO + (G == 2 ? (t & 1) * D : 0), tmem + kBn * (t & 1), sv + vs * C::kTile, id_o, t < G);
+        if (now) scores(t + 2);  // runs after P V, which reads these columns
         umma_commit(&o_done[t & 1]);
         umma_commit(&v_free[vs]);
       }
       __syncwarp();
+      if (more && !now) {
+        ok = warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) scores(t + 2);
+      }
+      __syncwarp();
       if (++vs == ST) vs = 0, vp ^= 1;
-      if (t + 2 < nt) ok = scores(t + 2);  // runs after P V, which reads these columns
+      if (more) next_k();
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -202,6 +216,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     const float2 c2 = make_float2(c, c);
     float m = 0.f;  // reference of the row (log2), once l > 0
     float l = 0.f;  // sum of P
+    constexpr int kPart = G == 2 ? 32 : 64;  // columns in registers at a time (at most 80 or 128 registers)
     bool ok = true;
     int s = g;
     uint32_t parity = 0;
@@ -215,28 +230,30 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       const float value = bl.value;
       const float* line = bl.line + 127 - row;
       const int live = nk - (t0 + t) * kBn;  // columns of the tile that are keys
-      uint32_t w[16];                        // P of the first half
-      // one half of the tile: of one bucket or not, with keys missing or not
-      auto half = [&](auto second_, auto flat_, auto cut_) {
-        constexpr int c0 = decltype(second_)::value ? 32 : 0;
+      uint32_t w[kPart / 2];                 // P of the first part
+      // one part of the tile: of one bucket or not, with keys missing or not
+      auto part = [&](auto second_, auto flat_, auto cut_) {
+        constexpr int c0 = decltype(second_)::value ? kPart : 0;
+        constexpr bool kLast = c0 + kPart == kBn;  // every score of the tile is in registers
         constexpr bool kFlat = decltype(flat_)::value, kCut = decltype(cut_)::value;
-        uint32_t u[32];
-        tmem_ld32(buf + c0, u);
+        uint32_t u[kPart];
+#pragma unroll
+        for (int e = 0; e < kPart; e += 32) tmem_ld32(buf + c0 + e, u + e);
         tmem_wait_ld_keep(u);
-        float x[32];  // S c + bias - m
+        float x[kPart];  // S c + bias - m
         const float off = kFlat ? value - m : -m;
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
+        for (int k = 0; k < kPart; k += 2) {
           float2 y = make_float2(off, off);
           if (!kFlat) y = __fadd2_rn(make_float2(line[c0 + k], line[c0 + k + 1]), y);
           y = __ffma2_rn(make_float2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), c2, y);
           x[k] = !kCut || c0 + k < live ? y.x : -INFINITY;
           x[k + 1] = !kCut || c0 + k + 1 < live ? y.y : -INFINITY;
         }
-        float tops[2] = {-INFINITY, -INFINITY};
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) tops[k / 2 % 2] = max3(tops[k / 2 % 2], x[k], x[k + 1]);
-        const float top = fmaxf(tops[0], tops[1]);
+        for (int k = 0; k < kPart; k += 2) tops[k / 2 % 4] = max3(tops[k / 2 % 4], x[k], x[k + 1]);
+        const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
         const bool move = l == 0.f ? top > -INFINITY : top > kSlack;
         if (__any_sync(0xffffffffu, move)) {
           // by whole powers of two, so that what is there already is rescaled without rounding
@@ -245,11 +262,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
           m += step;
           l *= alpha;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] -= step;
+          for (int k = 0; k < kPart; ++k) x[k] -= step;
           if (c0) {
             const uint32_t a2 = pack2<T>(alpha, alpha);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = mul2<T>(w[k], a2);
+            for (int k = 0; k < kPart / 2; ++k) w[k] = mul2<T>(w[k], a2);
           }
           if (t >= G) {  // (the group's sums so far: complete before these scores were, or waited for)
             if (G == 1 && !warp_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, a.ctx, kErrAttnSoftmax)) return false;
@@ -265,28 +282,34 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
             }
           }
         }
-        if (c0) tmem_st16(buf, w);  // (every score of the tile is in registers)
+        if (c0) {
+#pragma unroll
+          for (int e = 0; e < kPart / 2; e += 16) tmem_st16(buf + e, w + e);
+        }
         float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 32; e += 16) {
+        for (int e = 0; e < kPart; e += 16) {
           uint32_t v[8];
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
             const float2 p = make_float2(ex2(x[e + k]), ex2(x[e + k + 1]));
             acc = __fadd2_rn(acc, p);
-            (c0 ? v[k / 2] : w[e / 2 + k / 2]) = pack2<T>(p.x, p.y);
+            (kLast ? v[k / 2] : w[e / 2 + k / 2]) = pack2<T>(p.x, p.y);
           }
-          if (c0) tmem_st8(buf + 16 + e / 2, v);
+          if (kLast) tmem_st8(buf + (c0 + e) / 2, v);
         }
         l += acc.x + acc.y;
         return true;
       };
+      auto tile = [&](auto flat_, auto cut_) {
+        return part(std::false_type{}, flat_, cut_) && (kPart == kBn || part(std::true_type{}, flat_, cut_));
+      };
       using Yes = std::true_type;
       using No = std::false_type;
       if (live >= kBn)
-        ok = flat ? half(No{}, Yes{}, No{}) && half(Yes{}, Yes{}, No{}) : half(No{}, No{}, No{}) && half(Yes{}, No{}, No{});
+        ok = flat ? tile(Yes{}, No{}) : tile(No{}, No{});
       else
-        ok = flat ? half(No{}, Yes{}, Yes{}) && half(Yes{}, Yes{}, Yes{}) : half(No{}, No{}, Yes{}) && half(Yes{}, No{}, Yes{});
+        ok = flat ? tile(Yes{}, Yes{}) : tile(No{}, Yes{});
       if (!ok) break;
       tmem_wait_st();
       tc_fence_before();

@@ -23,8 +23,8 @@ constexpr int kRows = 16;
 
 template <int D>
 struct TokCfg {
-  static constexpr int ST = D == 32 ? 8 : (D == 64 ? 6 : 4);
-  static constexpr int CTAS = D == 128 ? 1 : 2;
+  static constexpr int ST = D == 32 ? 4 : 3;       // pieces of a warp's ring
+  static constexpr int CTAS = D == 128 ? 2 : 4;    // per SM: warps hide each other's latencies
   static constexpr int kTile = kPiece * D * 2;
   static constexpr int kWarpBytes = ST * 2 * kTile;
   static constexpr int SMEM = kWarps * kWarpBytes;
@@ -57,7 +57,7 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
 
 template <class T, int D>
 __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
-    attn_token_kernel(const __grid_constant__ BiasAttnArgs a, Split sp, int blocks, int chunk) {
+    attn_token_kernel(const __grid_constant__ BiasAttnArgs a, Split sp, int blocks) {
   using C = TokCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qc = lane & 3;
@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
   const int first_tok = r0 / group, last_tok = min((r0 + kRows - 1) / group, a.Lq - 1);
   int nk = first_tok < sl.nq ? sl.nk : 0;
   if (a.causal) nk = min(nk, max(0, sl.start + min(last_tok + 1, sl.nq)));
+  // the sequence's keys in sp.n equal parts of whole rounds of the warps
+  const int chunk = (sl.nk + sp.n * kPiece * kWarps - 1) / (sp.n * kPiece * kWarps) * (kPiece * kWarps);
   const int j_lo = min(split * chunk, nk), j_hi = min(j_lo + chunk, nk);
 
   // q fragments: lane (gr, qc) holds channels 16 k + 2 qc, + 1 (and + 8) of rows gr and gr + 8
@@ -280,15 +282,15 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   float total = 0.f, v[D / 32];
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) v[k] = 0.f;
-  if (top > -INFINITY && !nan)
-    for (int s = 0; s < sp.n; ++s) {
-      const float lse = sp.lse[s * rows + r];
-      if (lse == -INFINITY) continue;  // a part without a visible key
-      const float w = ex2(lse - top);
+  if (top > -INFINITY && !nan) {
+#pragma unroll 4
+    for (int s = 0; s < sp.n; ++s) {  // (a part without a visible key is zeros with weight 0)
+      const float w = ex2(sp.lse[s * rows + r] - top);
       total += w;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) v[k] = fmaf(w, sp.o[(s * rows + r) * D + lane + 32 * k], v[k]);
     }
+  }
   const int i = (int)(r % a.Lq), h = (int)(r / a.Lq % a.hq), b = (int)(r / a.Lq / a.hq);
   if (nan) total = top = __int_as_float(0x7fffffff);
   const float inv = total > 0.f || nan ? 1.f / total : 0.f;
@@ -298,30 +300,26 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   if (lane == 0) a.lse[r] = top > -INFINITY || nan ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
-// Parts of the keys: enough CTAs for four waves of what is resident (sequences
+// Parts of the keys: enough CTAs for two waves of what is resident (sequences
 // have unequal lengths), at least 256 keys (four pieces of every warp) in each.
-void token_plan(const BiasAttnArgs& a, int* blocks, int* n, int* chunk) {
+void token_plan(const BiasAttnArgs& a, int* blocks, int* n) {
   *blocks = (a.Lq * (a.hq / a.hk) + kRows - 1) / kRows;
   const long long ctas = (long long)a.B * a.hk * *blocks;
-  const long long want = 4LL * sm_count() * (a.d == 128 ? 1 : 2);
-  long long parts = (want + ctas - 1) / ctas;
-  const long long most = (a.Lk + 255) / 256;
-  parts = parts < 1 ? 1 : (parts > most ? most : parts);
-  const long long step = (a.Lk + parts - 1) / parts;
-  *chunk = (int)((step + 63) / 64 * 64);
-  *n = (a.Lk + *chunk - 1) / *chunk;
+  const long long want = 2LL * sm_count() * (a.d == 128 ? TokCfg<128>::CTAS : TokCfg<64>::CTAS);
+  const long long parts = want / ctas, most = (a.Lk + 255) / 256;
+  *n = (int)(parts < 1 ? 1 : (parts > most ? most : parts));
 }
 
 template <class T, int D>
 cudaError_t token(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
   using C = TokCfg<D>;
-  int blocks, n, chunk;
-  token_plan(a, &blocks, &n, &chunk);
+  int blocks, n;
+  token_plan(a, &blocks, &n);
   cudaError_t e = cudaFuncSetAttribute(attn_token_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const Split sp = split_of(a, n, scratch);
   prof_begin(kKindOther, st);
-  attn_token_kernel<T, D><<<(unsigned)((long long)a.B * a.hk * blocks * n), 32 * kWarps, C::SMEM, st>>>(a, sp, blocks, chunk);
+  attn_token_kernel<T, D><<<(unsigned)((long long)a.B * a.hk * blocks * n), 32 * kWarps, C::SMEM, st>>>(a, sp, blocks);
   prof_end(kKindOther, st);
   count_launch();
   e = cudaGetLastError();
@@ -357,8 +355,8 @@ template cudaError_t launch_attention_join<__half, 128>(const BiasAttnArgs&, con
 bool token_form(const BiasAttnArgs& a) { return (long long)a.Lq * (a.hq / a.hk) <= 64; }
 
 int token_splits(const BiasAttnArgs& a) {
-  int blocks, n, chunk;
-  token_plan(a, &blocks, &n, &chunk);
+  int blocks, n;
+  token_plan(a, &blocks, &n);
   return n;
 }
 
