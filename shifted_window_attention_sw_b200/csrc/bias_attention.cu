@@ -10,15 +10,14 @@
 // lse = -inf. Head h reads key head h * hk / hq.
 //
 // attn_fwd_kernel: one CTA per 128 query rows of a head, two CTAs per SM. The
-// keys go by in tiles of 64: S = Q K^T on tcgen05 into one of two TMEM buffers
-// (fp32), four softmax warps (TMEM lane = query row) turn it into P (16 bits,
-// written over the scores, the A operand of a TS MMA) and O += P V accumulates
-// in TMEM. D = 32 and 64: two groups of four warps take the tiles in turns, each
-// with its own buffer, softmax statistics and sums, joined at the end (sixteen
-// softmax warps per SM keep the exponentials busy while other warps wait for
-// their scores); D = 128, whose sums leave no room for a second set: one group,
-// and the scores of the next tile run while it works. One warp brings K and V
-// tiles (two or three stages, TMA; a tile in which the keys end goes by cp.async
+// keys go by in tiles: S = Q K^T on tcgen05 into TMEM (fp32), four softmax warps
+// (TMEM lane = query row) turn it into P (16 bits, written over the scores, the
+// A operand of a TS MMA) and O += P V accumulates in TMEM. D = 32 and 64: tiles
+// of 64 keys, which two groups of four warps take in turns, each with its own
+// score buffer, softmax statistics and sums, joined at the end (sixteen softmax
+// warps per SM). D = 128: one group and tiles of 128 keys, since the MMAs are the
+// bound and read half the shared memory per product of what 64-key tiles do. One
+// warp brings K and V tiles (TMA; a tile in which the keys end goes by cp.async
 // instead, so that nothing behind the lengths is read), one prepares each tile's
 // bias.
 //
@@ -27,12 +26,12 @@
 // consecutive banks); the causal rule is part of the line (-inf). Tiles of one
 // bucket (all far ones) skip the line: one value for the whole tile.
 //
-// Softmax in one pass over the keys (half a tile at a time with two groups): P is formed against
-// the row's reference m, the maximum as it was when it last moved. Only when a
-// score exceeds m by more than kSlack (in log2) does the warp raise m, by a whole
-// number, and rescale what it has by that power of two (without rounding); P is
-// at most 2^kSlack, exact in fp32 sums and finite in 16 bits, and o and lse do
-// not depend on m. TMEM columns: scores [0, 64) and [64, 128), O behind.
+// Softmax in one pass over the keys, half a tile in registers at a time: P is
+// formed against the row's reference m, the maximum as it was when it last
+// moved. Only when a score exceeds m by more than kSlack (in log2) does the warp
+// raise m, by a whole number, and rescale what it has by that power of two
+// (without rounding); P is at most 2^kSlack, exact in fp32 sums and finite in 16
+// bits, and o and lse do not depend on m. TMEM columns: scores first, O behind.
 //
 // Bound: one exponential per visible pair (16 per clock and SM) for D = 32 and
 // 64, the tensor cores for D = 128.
@@ -45,26 +44,27 @@ namespace {
 constexpr int kProducerWarps = 2;
 constexpr float kSlack = 8.f;
 
-constexpr int kBn = 64;           // keys per tile
-constexpr int kLineN = 127 + kBn;  // offsets in a tile
 
 
 template <int D>
 struct FwdCfg {
-  static constexpr int G = D == 128 ? 1 : 2;   // groups of four softmax warps, each with its own sums O
+  static constexpr int G = D == 128 ? 1 : 2;     // groups of four softmax warps, each with its own sums O
+  static constexpr int BN = D == 128 ? 128 : 64;  // keys per tile
+  static constexpr int NBUF = D == 128 ? 1 : 2;   // score buffers
+  static constexpr int ST = D == 128 ? 1 : 3;     // stages of K and V: two CTAs share 227 KB
   static constexpr int kMmaWarp = 4 * G;
   static constexpr int THREADS = 32 * (4 * G + 1 + kProducerWarps);
-  static constexpr int ST = D == 128 ? 2 : 3;  // stages: two CTAs share 227 KB
-  using Line = BiasLine<kLineN, false>;
-  static constexpr int kTile = kBn * D * 2;
+  static constexpr int kLineN = 127 + BN;         // offsets in a tile
+  using Line = BiasLine<kLineN, false>;           // two stages
+  static constexpr int kTile = BN * D * 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 128 * D * 2;
   static constexpr int OFF_V = OFF_K + ST * kTile;
   static constexpr int OFF_BIAS = OFF_V + ST * kTile;
-  static constexpr int OFF_BAR = OFF_BIAS + (ST * (int)sizeof(Line) + 15) / 16 * 16;
+  static constexpr int OFF_BAR = OFF_BIAS + (2 * (int)sizeof(Line) + 15) / 16 * 16;
   static constexpr int OFF_ML = OFF_BAR + 256;  // [G][128] (m, l) of the groups' rows
   static constexpr int SMEM = OFF_ML + (G == 2 ? 2 * 128 * 8 : 0);
-  static constexpr int kColO = 2 * kBn;
+  static constexpr int kColO = NBUF * BN;
   static constexpr uint32_t kTmem = 256;
   static_assert(kColO + G * D <= 256, "TMEM columns of a CTA");
 };
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   const BiasAttnArgs& a = params.a;
   using C = FwdCfg<D>;
   using Line = typename C::Line;
-  constexpr int ST = C::ST, G = C::G, kMmaWarp = C::kMmaWarp;
+  constexpr int ST = C::ST, G = C::G, NBUF = C::NBUF, kBn = C::BN, kMmaWarp = C::kMmaWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   Line* lines = reinterpret_cast<Line*>(smem + C::OFF_BIAS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   uint64_t* k_free = bars + ST;       // [ST]
   uint64_t* v_full = bars + 2 * ST;   // [ST]
   uint64_t* v_free = bars + 3 * ST;   // [ST]
-  uint64_t* s_full = bars + 4 * ST;   // [ST] bias line written and scores in TMEM
-  uint64_t* p_full = bars + 5 * ST;   // [2] P written over them
+  uint64_t* s_full = bars + 4 * ST;   // [2] bias line written and scores in TMEM
+  uint64_t* p_full = s_full + 2;      // [2] P written over them
   uint64_t* o_done = p_full + 2;      // [2] P V accumulated
   uint64_t* q_full = p_full + 4;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(p_full + 5);
@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       mbar_init(&k_free[k], 1);
       mbar_init(&v_full[k], 1);
       mbar_init(&v_free[k], 1);
-      mbar_init(&s_full[k], 2);
     }
     for (int k = 0; k < 2; ++k) {
+      mbar_init(&s_full[k], 2);
       mbar_init(&p_full[k], 4);
       mbar_init(&o_done[k], 1);
     }
@@ -151,12 +151,12 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
         if (++s == ST) s = 0, parity ^= 1;
       }
     } else if (nt > 0) {
-      const LineWriter<T, kLineN, false> writer(a, h);
+      const LineWriter<T, C::kLineN, false> writer(a, h);
       for (int t = 0; t < nt; ++t) {
-        if (t >= ST && !warp_wait(&v_free[s], parity, a.ctx, kErrAttnLoad)) break;  // (P V follows every read of the line)
-        writer.write(&lines[s], (t0 + t) * kBn - pos0 - 127);
-        if (lane == 0) mbar_arrive(&s_full[s]);
-        if (++s == ST) s = 0, parity ^= 1;
+        // P V of a tile follows every read of its line
+        if (t >= 2 && !warp_wait(&o_done[t & 1], ((t >> 1) - 1) & 1, a.ctx, kErrAttnLoad)) break;
+        writer.write(&lines[t & 1], (t0 + t) * kBn - pos0 - 127);
+        if (lane == 0) mbar_arrive(&s_full[t & 1]);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -167,15 +167,15 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     int ks = 0, vs = 0;
     uint32_t kp = 0, vp = 0;
     auto scores = [&](int t) {  // by the elected lane
-      mma_rows<D, kBn>(tmem + kBn * (t & 1), sq, sk + ks * C::kTile, id_s);
-      umma_commit(&s_full[ks]);
+      mma_rows<D, kBn>(tmem + kBn * (t % NBUF), sq, sk + ks * C::kTile, id_s);
+      umma_commit(&s_full[t & 1]);
       umma_commit(&k_free[ks]);
     };
     auto next_k = [&]() {
       if (++ks == ST) ks = 0, kp ^= 1;
     };
     bool ok = nt > 0 && warp_wait(q_full, 0, a.ctx, kErrAttnMma);
-    for (int t = 0; t < 2 && t < nt && ok; ++t) {
+    for (int t = 0; t < NBUF && t < nt && ok; ++t) {
       ok = warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma);
       if (!ok) break;
       tc_fence_after();
@@ -184,15 +184,15 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       next_k();
     }
     for (int t = 0; t < nt && ok; ++t) {
-      const bool more = t + 2 < nt;
+      const bool more = t + NBUF < nt;
       ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t & 1], (t >> 1) & 1, a.ctx, kErrAttnMma);
       if (!ok) break;
       // the scores that follow go out at once when their keys are there
       const bool now = more && __all_sync(0xffffffffu, mbar_test(&k_full[ks], kp));
       tc_fence_after();
       if (elect_one()) {
-        mma_acc<D, kBn>(tmem + C::kColO + (G == 2 ? (t & 1) * D : 0), tmem + kBn * (t & 1), sv + vs * C::kTile, id_o, t < G);
-        if (now) scores(t + 2);  // runs after P V, which reads these columns
+        mma_acc<D, kBn>(tmem + C::kColO + (G == 2 ? (t & 1) * D : 0), tmem + kBn * (t % NBUF), sv + vs * C::kTile, id_o, t < G);
+        if (now) scores(t + NBUF);  // runs after P V, which reads these columns
         umma_commit(&o_done[t & 1]);
         umma_commit(&v_free[vs]);
       }
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
         ok = warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) scores(t + 2);
+        if (elect_one()) scores(t + NBUF);
       }
       __syncwarp();
       if (++vs == ST) vs = 0, vp ^= 1;
@@ -216,25 +216,21 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     const float2 c2 = make_float2(c, c);
     float m = 0.f;  // reference of the row (log2), once l > 0
     float l = 0.f;  // sum of P
-    constexpr int kPart = G == 2 ? 32 : 64;  // columns in registers at a time (at most 80 or 128 registers)
+    constexpr int kPart = kBn / 2;  // columns in registers at a time (80 or 128 registers)
     bool ok = true;
-    int s = g;
-    uint32_t parity = 0;
     for (int t = g; t < nt; t += G) {
-      ok = warp_wait(&s_full[s], parity, a.ctx, kErrAttnSoftmax);
+      ok = warp_wait(&s_full[t & 1], (t >> 1) & 1, a.ctx, kErrAttnSoftmax);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t buf = tw + kBn * (t & 1);
-      const Line& bl = lines[s];
+      const uint32_t buf = tw + kBn * (t % NBUF);
+      const Line& bl = lines[t & 1];
       const bool flat = bl.flat != 0;
       const float value = bl.value;
       const float* line = bl.line + 127 - row;
       const int live = nk - (t0 + t) * kBn;  // columns of the tile that are keys
-      uint32_t w[kPart / 2];                 // P of the first part
       // one part of the tile: of one bucket or not, with keys missing or not
       auto part = [&](auto second_, auto flat_, auto cut_) {
         constexpr int c0 = decltype(second_)::value ? kPart : 0;
-        constexpr bool kLast = c0 + kPart == kBn;  // every score of the tile is in registers
         constexpr bool kFlat = decltype(flat_)::value, kCut = decltype(cut_)::value;
         uint32_t u[kPart];
 #pragma unroll
@@ -265,8 +261,16 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
           for (int k = 0; k < kPart; ++k) x[k] -= step;
           if (c0) {
             const uint32_t a2 = pack2<T>(alpha, alpha);
+            tmem_wait_st();
 #pragma unroll
-            for (int k = 0; k < kPart / 2; ++k) w[k] = mul2<T>(w[k], a2);
+            for (int e = 0; e < c0 / 2; e += 8) {
+              uint32_t r[8];
+              tmem_ld8(buf + e, r);
+              tmem_wait_ld_keep(r);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) r[k] = mul2<T>(r[k], a2);
+              tmem_st8(buf + e, r);
+            }
           }
           if (t >= G) {  // (the group's sums so far: complete before these scores were, or waited for)
             if (G == 1 && !warp_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, a.ctx, kErrAttnSoftmax)) return false;
@@ -282,10 +286,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
             }
           }
         }
-        if (c0) {
-#pragma unroll
-          for (int e = 0; e < kPart / 2; e += 16) tmem_st16(buf + e, w + e);
-        }
         float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < kPart; e += 16) {
@@ -294,9 +294,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
           for (int k = 0; k < 16; k += 2) {
             const float2 p = make_float2(ex2(x[e + k]), ex2(x[e + k + 1]));
             acc = __fadd2_rn(acc, p);
-            (kLast ? v[k / 2] : w[e / 2 + k / 2]) = pack2<T>(p.x, p.y);
+            v[k / 2] = pack2<T>(p.x, p.y);
           }
-          if (kLast) tmem_st8(buf + (c0 + e) / 2, v);
+          tmem_st8(buf + (c0 + e) / 2, v);  // over scores that have been read
         }
         l += acc.x + acc.y;
         return true;
@@ -315,8 +315,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[t & 1]);
-      s += G;
-      if (s >= ST) s -= ST, parity ^= 1;
     }
     const int last = nt - 1 - (G == 2 ? (nt - 1 - g) & 1 : 0);  // the group's last tile
     if (ok && last >= 0) ok = warp_wait(&o_done[last & 1], (last >> 1) & 1, a.ctx, kErrAttnSoftmax);
@@ -389,10 +387,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
 }
 
 // Parts of the keys when the query tiles alone leave SMs idle: as many as fill
-// two CTAs per SM, at least eight key tiles in each.
+// two CTAs per SM, at least 512 keys in each.
 int forward_splits(const BiasAttnArgs& a) {
   const long long ctas = (long long)a.B * a.hq * ((a.Lq + 127) / 128), slots = 2LL * sm_count();
-  const long long tiles = (a.Lk + kBn - 1) / kBn;
+  const long long tiles = (a.Lk + 63) / 64;
   if (2 * ctas > slots) return 1;
   const long long parts = slots / ctas, most = tiles / 8;
   return (int)(parts < most ? parts : (most < 1 ? 1 : most));
@@ -409,8 +407,8 @@ cudaError_t forward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
   FwdParams params;
   params.a = a;
   make_head_map(&params.q, a.q, a.B, a.Lq, a.hq, D, dtype, 128);
-  make_head_map(&params.k, a.k, a.B, a.Lk, a.hk, D, dtype, kBn);
-  make_head_map(&params.v, a.v, a.B, a.Lk, a.hk, D, dtype, kBn);
+  make_head_map(&params.k, a.k, a.B, a.Lk, a.hk, D, dtype, C::BN);
+  make_head_map(&params.v, a.v, a.B, a.Lk, a.hk, D, dtype, C::BN);
   const long long grid = (long long)a.B * a.hq * ((a.Lq + 127) / 128) * sp.n;
   prof_begin(kKindOther, st);
   attn_fwd_kernel<T, D><<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(params, sp);
