@@ -50,7 +50,8 @@ template <int D>
 struct FwdCfg {
   static constexpr int G = D == 128 ? 1 : 2;     // groups of four softmax warps, each with its own sums O
   static constexpr int BN = D == 128 ? 128 : 64;  // keys per tile
-  static constexpr int NBUF = D == 128 ? 1 : 2;   // score buffers
+  static constexpr int NBUF = D == 128 ? 1 : (D == 64 ? 2 : 3);  // score buffers: what TMEM holds
+  static constexpr int RING = NBUF < 2 ? 2 : NBUF;               // barriers of the scores
   static constexpr int ST = D == 128 ? 1 : 3;     // stages of K and V: two CTAs share 227 KB
   static constexpr int kMmaWarp = 4 * G;
   static constexpr int THREADS = 32 * (4 * G + 1 + kProducerWarps);
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   const BiasAttnArgs& a = params.a;
   using C = FwdCfg<D>;
   using Line = typename C::Line;
-  constexpr int ST = C::ST, G = C::G, NBUF = C::NBUF, kBn = C::BN, kMmaWarp = C::kMmaWarp;
+  constexpr int ST = C::ST, G = C::G, NBUF = C::NBUF, RING = C::RING, kBn = C::BN, kMmaWarp = C::kMmaWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   Line* lines = reinterpret_cast<Line*>(smem + C::OFF_BIAS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -87,11 +88,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   uint64_t* k_free = bars + ST;       // [ST]
   uint64_t* v_full = bars + 2 * ST;   // [ST]
   uint64_t* v_free = bars + 3 * ST;   // [ST]
-  uint64_t* s_full = bars + 4 * ST;   // [2] bias line written and scores in TMEM
-  uint64_t* p_full = s_full + 2;      // [2] P written over them
-  uint64_t* o_done = p_full + 2;      // [2] P V accumulated
-  uint64_t* q_full = p_full + 4;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(p_full + 5);
+  uint64_t* s_full = bars + 4 * ST;   // [RING] bias line written and scores in TMEM
+  uint64_t* p_full = s_full + RING;   // [4] P written over them (a group may be two tiles ahead of the MMAs)
+  uint64_t* o_done = p_full + 4;      // [2] P V accumulated
+  uint64_t* q_full = o_done + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_full + 1);
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -118,11 +119,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       mbar_init(&v_full[k], 1);
       mbar_init(&v_free[k], 1);
     }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(&s_full[k], 2);
-      mbar_init(&p_full[k], 4);
-      mbar_init(&o_done[k], 1);
-    }
+    for (int k = 0; k < RING; ++k) mbar_init(&s_full[k], 2);
+    for (int k = 0; k < 4; ++k) mbar_init(&p_full[k], 4);
+    for (int k = 0; k < 2; ++k) mbar_init(&o_done[k], 1);
     mbar_init(q_full, 1);
     fence_mbar_init();
   }
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
         // P V of a tile follows every read of its line
         if (t >= 2 && !warp_wait(&o_done[t & 1], ((t >> 1) - 1) & 1, a.ctx, kErrAttnLoad)) break;
         writer.write(&lines[t & 1], (t0 + t) * kBn - pos0 - 127);
-        if (lane == 0) mbar_arrive(&s_full[t & 1]);
+        if (lane == 0) mbar_arrive(&s_full[t % RING]);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -168,7 +167,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     uint32_t kp = 0, vp = 0;
     auto scores = [&](int t) {  // by the elected lane
       mma_rows<D, kBn>(tmem + kBn * (t % NBUF), sq, sk + ks * C::kTile, id_s);
-      umma_commit(&s_full[t & 1]);
+      umma_commit(&s_full[t % RING]);
       umma_commit(&k_free[ks]);
     };
     auto next_k = [&]() {
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     }
     for (int t = 0; t < nt && ok; ++t) {
       const bool more = t + NBUF < nt;
-      ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t & 1], (t >> 1) & 1, a.ctx, kErrAttnMma);
+      ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t & 3], (t >> 2) & 1, a.ctx, kErrAttnMma);
       if (!ok) break;
       // the scores that follow go out at once when their keys are there
       const bool now = more && __all_sync(0xffffffffu, mbar_test(&k_full[ks], kp));
@@ -219,7 +218,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     constexpr int kPart = kBn / 2;  // columns in registers at a time (80 or 128 registers)
     bool ok = true;
     for (int t = g; t < nt; t += G) {
-      ok = warp_wait(&s_full[t & 1], (t >> 1) & 1, a.ctx, kErrAttnSoftmax);
+      ok = warp_wait(&s_full[t % RING], (t / RING) & 1, a.ctx, kErrAttnSoftmax);
       if (!ok) break;
       tc_fence_after();
       const uint32_t buf = tw + kBn * (t % NBUF);
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t & 1]);
+      if (lane == 0) mbar_arrive(&p_full[t & 3]);
     }
     const int last = nt - 1 - (G == 2 ? (nt - 1 - g) & 1 : 0);  // the group's last tile
     if (ok && last >= 0) ok = warp_wait(&o_done[last & 1], (last >> 1) & 1, a.ctx, kErrAttnSoftmax);

@@ -219,9 +219,30 @@ __device__ __forceinline__ void bring_tile(uint32_t dst, const HeadMap& m, const
   }
 }
 
-// A whole warp waits; false in every lane when any lane's wait gave up.
+// A whole warp waits; false in every lane when the wait gave up (as mbar_wait
+// does). The hardware suspends the warp for up to the hint (ns) per try: waiting
+// warps that poll more often take issue slots from the working ones.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtx& ctx, int code) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx.err, code, ctx.wait_limit));
+  auto once = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return __all_sync(0xffffffffu, ok != 0);
+  };
+  if (once()) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!once()) {
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > ctx.wait_limit)) {
+      if ((threadIdx.x & 31) == 0) atomicCAS(ctx.err, 0, code);
+      return false;
+    }
+  }
+  return true;
 }
 
 // One lane of a converged warp, which the compiler knows to be one: MMAs issued
