@@ -42,6 +42,7 @@ namespace vswin {
 namespace {
 
 constexpr int kProducerWarps = 2;
+constexpr int kRing = 4;         // bias lines, and the barriers of scores and P
 constexpr float kSlack = 8.f;
 
 
@@ -51,18 +52,17 @@ struct FwdCfg {
   static constexpr int G = D == 128 ? 1 : 2;     // groups of four softmax warps, each with its own sums O
   static constexpr int BN = D == 128 ? 128 : 64;  // keys per tile
   static constexpr int NBUF = D == 128 ? 1 : (D == 64 ? 2 : 3);  // score buffers: what TMEM holds
-  static constexpr int RING = NBUF < 2 ? 2 : NBUF;               // barriers of the scores
   static constexpr int ST = D == 128 ? 1 : 3;     // stages of K and V: two CTAs share 227 KB
   static constexpr int kMmaWarp = 4 * G;
   static constexpr int THREADS = 32 * (4 * G + 1 + kProducerWarps);
   static constexpr int kLineN = 127 + BN;         // offsets in a tile
-  using Line = BiasLine<kLineN, false>;           // two stages
+  using Line = BiasLine<kLineN, false>;           // kRing stages
   static constexpr int kTile = BN * D * 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 128 * D * 2;
   static constexpr int OFF_V = OFF_K + ST * kTile;
   static constexpr int OFF_BIAS = OFF_V + ST * kTile;
-  static constexpr int OFF_BAR = OFF_BIAS + (2 * (int)sizeof(Line) + 15) / 16 * 16;
+  static constexpr int OFF_BAR = OFF_BIAS + (kRing * (int)sizeof(Line) + 15) / 16 * 16;
   static constexpr int OFF_ML = OFF_BAR + 256;  // [G][128] (m, l) of the groups' rows
   static constexpr int SMEM = OFF_ML + (G == 2 ? 2 * 128 * 8 : 0);
   static constexpr int kColO = NBUF * BN;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   const BiasAttnArgs& a = params.a;
   using C = FwdCfg<D>;
   using Line = typename C::Line;
-  constexpr int ST = C::ST, G = C::G, NBUF = C::NBUF, RING = C::RING, kBn = C::BN, kMmaWarp = C::kMmaWarp;
+  constexpr int ST = C::ST, G = C::G, NBUF = C::NBUF, kBn = C::BN, kMmaWarp = C::kMmaWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   Line* lines = reinterpret_cast<Line*>(smem + C::OFF_BIAS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -88,9 +88,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   uint64_t* k_free = bars + ST;       // [ST]
   uint64_t* v_full = bars + 2 * ST;   // [ST]
   uint64_t* v_free = bars + 3 * ST;   // [ST]
-  uint64_t* s_full = bars + 4 * ST;   // [RING] bias line written and scores in TMEM
-  uint64_t* p_full = s_full + RING;   // [4] P written over them (a group may be two tiles ahead of the MMAs)
-  uint64_t* o_done = p_full + 4;      // [2] P V accumulated
+  uint64_t* s_full = bars + 4 * ST;   // [kRing] bias line written and scores in TMEM
+  uint64_t* p_full = s_full + kRing;  // [kRing] line read and P written over the scores
+  uint64_t* o_done = p_full + kRing;  // [2] P V accumulated
   uint64_t* q_full = o_done + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_full + 1);
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
@@ -119,8 +119,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       mbar_init(&v_full[k], 1);
       mbar_init(&v_free[k], 1);
     }
-    for (int k = 0; k < RING; ++k) mbar_init(&s_full[k], 2);
-    for (int k = 0; k < 4; ++k) mbar_init(&p_full[k], 4);
+    for (int k = 0; k < kRing; ++k) {
+      mbar_init(&s_full[k], 2);
+      mbar_init(&p_full[k], 4);
+    }
     for (int k = 0; k < 2; ++k) mbar_init(&o_done[k], 1);
     mbar_init(q_full, 1);
     fence_mbar_init();
@@ -137,25 +139,29 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   if (warp > kMmaWarp) {
     // ------------------------------------------------------------ producers: tiles, bias lines
     const uint32_t sq = smem_u32(smem + C::OFF_Q), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
-    int s = 0;
-    uint32_t parity = 1;  // of the stage's previous use
     if (warp == kMmaWarp + 1) {
       if (nt > 0) bring_tile<T, D, 128>(sq, params.q, a.q, b, h, i0, sl.nq, a.Lq, q_full);
-      for (int t = 0; t < nt; ++t) {
-        const int j0 = (t0 + t) * kBn;
-        if (t >= ST && !warp_wait(&k_free[s], parity, a.ctx, kErrAttnLoad)) break;
-        bring_tile<T, D, kBn>(sk + s * C::kTile, params.k, a.k, b, hk, j0, sl.nk, a.Lk, &k_full[s]);
-        if (t >= ST && !warp_wait(&v_free[s], parity, a.ctx, kErrAttnLoad)) break;
-        bring_tile<T, D, kBn>(sv + s * C::kTile, params.v, a.v, b, hk, j0, sl.nk, a.Lk, &v_full[s]);
-        if (++s == ST) s = 0, parity ^= 1;
+      // K runs a tile ahead of V: its stage is free a tile earlier
+      auto wait_stage = [&](uint64_t* freed, int t) {
+        return t < ST || warp_wait(&freed[t % ST], (t / ST - 1) & 1, a.ctx, kErrAttnLoad);
+      };
+      for (int t = 0; t <= nt; ++t) {
+        if (t < nt) {
+          if (!wait_stage(k_free, t)) break;
+          bring_tile<T, D, kBn>(sk + t % ST * C::kTile, params.k, a.k, b, hk, (t0 + t) * kBn, sl.nk, a.Lk, &k_full[t % ST]);
+        }
+        if (t > 0) {
+          const int u = t - 1;
+          if (!wait_stage(v_free, u)) break;
+          bring_tile<T, D, kBn>(sv + u % ST * C::kTile, params.v, a.v, b, hk, (t0 + u) * kBn, sl.nk, a.Lk, &v_full[u % ST]);
+        }
       }
     } else if (nt > 0) {
       const LineWriter<T, C::kLineN, false> writer(a, h);
       for (int t = 0; t < nt; ++t) {
-        // P V of a tile follows every read of its line
-        if (t >= 2 && !warp_wait(&o_done[t & 1], ((t >> 1) - 1) & 1, a.ctx, kErrAttnLoad)) break;
-        writer.write(&lines[t & 1], (t0 + t) * kBn - pos0 - 127);
-        if (lane == 0) mbar_arrive(&s_full[t % RING]);
+        if (t >= kRing && !warp_wait(&p_full[t % kRing], (t / kRing - 1) & 1, a.ctx, kErrAttnLoad)) break;
+        writer.write(&lines[t % kRing], (t0 + t) * kBn - pos0 - 127);
+        if (lane == 0) mbar_arrive(&s_full[t % kRing]);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     uint32_t kp = 0, vp = 0;
     auto scores = [&](int t) {  // by the elected lane
       mma_rows<D, kBn>(tmem + kBn * (t % NBUF), sq, sk + ks * C::kTile, id_s);
-      umma_commit(&s_full[t % RING]);
+      umma_commit(&s_full[t % kRing]);
       umma_commit(&k_free[ks]);
     };
     auto next_k = [&]() {
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     }
     for (int t = 0; t < nt && ok; ++t) {
       const bool more = t + NBUF < nt;
-      ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t & 3], (t >> 2) & 1, a.ctx, kErrAttnMma);
+      ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnMma);
       if (!ok) break;
       // the scores that follow go out at once when their keys are there
       const bool now = more && __all_sync(0xffffffffu, mbar_test(&k_full[ks], kp));
@@ -218,11 +224,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     constexpr int kPart = kBn / 2;  // columns in registers at a time (80 or 128 registers)
     bool ok = true;
     for (int t = g; t < nt; t += G) {
-      ok = warp_wait(&s_full[t % RING], (t / RING) & 1, a.ctx, kErrAttnSoftmax);
+      ok = warp_wait(&s_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnSoftmax);
       if (!ok) break;
       tc_fence_after();
       const uint32_t buf = tw + kBn * (t % NBUF);
-      const Line& bl = lines[t & 1];
+      const Line& bl = lines[t % kRing];
       const bool flat = bl.flat != 0;
       const float value = bl.value;
       const float* line = bl.line + 127 - row;
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t & 3]);
+      if (lane == 0) mbar_arrive(&p_full[t % kRing]);
     }
     const int last = nt - 1 - (G == 2 ? (nt - 1 - g) & 1 : 0);  // the group's last tile
     if (ok && last >= 0) ok = warp_wait(&o_done[last & 1], (last >> 1) & 1, a.ctx, kErrAttnSoftmax);
