@@ -84,14 +84,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   extern __shared__ __align__(1024) uint8_t smem[];
   Line* lines = reinterpret_cast<Line*>(smem + C::OFF_BIAS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* k_full = bars;            // [ST]
-  uint64_t* k_free = bars + ST;       // [ST]
-  uint64_t* v_full = bars + 2 * ST;   // [ST]
-  uint64_t* v_free = bars + 3 * ST;   // [ST]
-  uint64_t* s_full = bars + 4 * ST;   // [kRing] bias line written and scores in TMEM
-  uint64_t* p_full = s_full + kRing;  // [kRing] line read and P written over the scores
-  uint64_t* o_done = p_full + kRing;  // [2] P V accumulated
-  uint64_t* q_full = o_done + 2;
+  uint64_t* k_full = bars;            // [ST] K tile
+  uint64_t* s_full = bars + ST;       // [kRing] bias line written and scores in TMEM (K has been read)
+  uint64_t* p_full = s_full + kRing;  // [kRing] V tile, and P written over the scores (line and scores have been read)
+  uint64_t* o_done = p_full + kRing;  // [kRing] P V accumulated (V has been read)
+  uint64_t* q_full = o_done + kRing;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_full + 1);
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
 
@@ -113,17 +110,12 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   const int t0 = min(split * per, tiles), nt = min(t0 + per, tiles) - t0;
 
   if (tid == 0) {
-    for (int k = 0; k < ST; ++k) {
-      mbar_init(&k_full[k], 1);
-      mbar_init(&k_free[k], 1);
-      mbar_init(&v_full[k], 1);
-      mbar_init(&v_free[k], 1);
-    }
+    for (int k = 0; k < ST; ++k) mbar_init(&k_full[k], 1);
     for (int k = 0; k < kRing; ++k) {
       mbar_init(&s_full[k], 2);
-      mbar_init(&p_full[k], 4);
+      mbar_init(&p_full[k], 5);
+      mbar_init(&o_done[k], 1);
     }
-    for (int k = 0; k < 2; ++k) mbar_init(&o_done[k], 1);
     mbar_init(q_full, 1);
     fence_mbar_init();
   }
@@ -142,18 +134,18 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     if (warp == kMmaWarp + 1) {
       if (nt > 0) bring_tile<T, D, 128>(sq, params.q, a.q, b, h, i0, sl.nq, a.Lq, q_full);
       // K runs a tile ahead of V: its stage is free a tile earlier
-      auto wait_stage = [&](uint64_t* freed, int t) {
-        return t < ST || warp_wait(&freed[t % ST], (t / ST - 1) & 1, a.ctx, kErrAttnLoad);
+      auto wait_tile = [&](uint64_t* done, int t) {
+        return t < 0 || warp_wait(&done[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnLoad);
       };
       for (int t = 0; t <= nt; ++t) {
         if (t < nt) {
-          if (!wait_stage(k_free, t)) break;
+          if (!wait_tile(s_full, t - ST)) break;
           bring_tile<T, D, kBn>(sk + t % ST * C::kTile, params.k, a.k, b, hk, (t0 + t) * kBn, sl.nk, a.Lk, &k_full[t % ST]);
         }
         if (t > 0) {
           const int u = t - 1;
-          if (!wait_stage(v_free, u)) break;
-          bring_tile<T, D, kBn>(sv + u % ST * C::kTile, params.v, a.v, b, hk, (t0 + u) * kBn, sl.nk, a.Lk, &v_full[u % ST]);
+          if (!wait_tile(o_done, u - ST)) break;
+          bring_tile<T, D, kBn>(sv + u % ST * C::kTile, params.v, a.v, b, hk, (t0 + u) * kBn, sl.nk, a.Lk, &p_full[u % kRing]);
         }
       }
     } else if (nt > 0) {
@@ -169,48 +161,40 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     // (the whole warp waits, one elected lane issues)
     const uint32_t sq = smem_u32(smem + C::OFF_Q), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
     constexpr uint32_t id_s = idesc16<T>(128, kBn, 0, 0), id_o = idesc16<T>(128, D, 0, 1);
-    int ks = 0, vs = 0;
-    uint32_t kp = 0, vp = 0;
     auto scores = [&](int t) {  // by the elected lane
-      mma_rows<D, kBn>(tmem + kBn * (t % NBUF), sq, sk + ks * C::kTile, id_s);
+      mma_rows<D, kBn>(tmem + kBn * (t % NBUF), sq, sk + t % ST * C::kTile, id_s);
       umma_commit(&s_full[t % kRing]);
-      umma_commit(&k_free[ks]);
     };
-    auto next_k = [&]() {
-      if (++ks == ST) ks = 0, kp ^= 1;
-    };
+    auto wait_k = [&](int t) { return warp_wait(&k_full[t % ST], (t / ST) & 1, a.ctx, kErrAttnMma); };
     bool ok = nt > 0 && warp_wait(q_full, 0, a.ctx, kErrAttnMma);
     for (int t = 0; t < NBUF && t < nt && ok; ++t) {
-      ok = warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma);
+      ok = wait_k(t);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) scores(t);
       __syncwarp();
-      next_k();
     }
     for (int t = 0; t < nt && ok; ++t) {
-      const bool more = t + NBUF < nt;
-      ok = warp_wait(&v_full[vs], vp, a.ctx, kErrAttnMma) && warp_wait(&p_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnMma);
+      const int u = t + NBUF;  // the tile whose scores take this one's buffer
+      ok = warp_wait(&p_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnMma);
       if (!ok) break;
       // the scores that follow go out at once when their keys are there
-      const bool now = more && __all_sync(0xffffffffu, mbar_test(&k_full[ks], kp));
+      const bool now = u < nt && __all_sync(0xffffffffu, mbar_test(&k_full[u % ST], (u / ST) & 1));
       tc_fence_after();
       if (elect_one()) {
-        mma_acc<D, kBn>(tmem + C::kColO + (G == 2 ? (t & 1) * D : 0), tmem + kBn * (t % NBUF), sv + vs * C::kTile, id_o, t < G);
-        if (now) scores(t + NBUF);  // runs after P V, which reads these columns
-        umma_commit(&o_done[t & 1]);
-        umma_commit(&v_free[vs]);
+        mma_acc<D, kBn>(tmem + C::kColO + (G == 2 ? (t & 1) * D : 0), tmem + kBn * (t % NBUF), sv + t % ST * C::kTile, id_o,
+                        t < G);
+        umma_commit(&o_done[t % kRing]);
+        if (now) scores(u);  // runs after P V, which reads these columns
       }
       __syncwarp();
-      if (more && !now) {
-        ok = warp_wait(&k_full[ks], kp, a.ctx, kErrAttnMma);
+      if (u < nt && !now) {
+        ok = wait_k(u);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) scores(t + NBUF);
+        if (elect_one()) scores(u);
+        __syncwarp();
       }
-      __syncwarp();
-      if (++vs == ST) vs = 0, vp ^= 1;
-      if (more) next_k();
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -278,7 +262,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
             }
           }
           if (t >= G) {  // (the group's sums so far: complete before these scores were, or waited for)
-            if (G == 1 && !warp_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, a.ctx, kErrAttnSoftmax)) return false;
+            if (G == 1 && !warp_wait(&o_done[(t - 1) % kRing], ((t - 1) / kRing) & 1, a.ctx, kErrAttnSoftmax)) return false;
             tc_fence_after();
 #pragma unroll
             for (int e = 0; e < D; e += 8) {
@@ -322,7 +306,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       if (lane == 0) mbar_arrive(&p_full[t % kRing]);
     }
     const int last = nt - 1 - (G == 2 ? (nt - 1 - g) & 1 : 0);  // the group's last tile
-    if (ok && last >= 0) ok = warp_wait(&o_done[last & 1], (last >> 1) & 1, a.ctx, kErrAttnSoftmax);
+    if (ok && last >= 0) ok = warp_wait(&o_done[last % kRing], (last / kRing) & 1, a.ctx, kErrAttnSoftmax);
     tc_fence_after();
     // the groups' sums over their tiles of the row, weighed against the larger reference; a group without any has weight 0
     float weight[2] = {1.f, 0.f};
