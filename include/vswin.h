@@ -366,7 +366,7 @@ int vswin_bucket_map(int buckets, int max_distance, int bidirectional, int* map)
 
 /* The bias: table [buckets][hq] of the tensors' type, map int
  * [2 max_distance + 1] on the device (vswin_bucket_map's or any other), offsets
- * beyond max_distance read its ends. buckets up to 1024, max_distance up to
+ * beyond max_distance read its ends. buckets up to 512, max_distance up to
  * 2^20. A bias at or below -1e30 takes the key out of the softmax. A map entry
  * outside [0, buckets) counts as bias 0 and is reported by vswin_poll_error
  * (VSWIN_ERR_BOUNDS). */

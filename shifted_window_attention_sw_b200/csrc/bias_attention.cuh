@@ -151,10 +151,10 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_addr, uint3
     umma_ss(d_tmem, da + ((piece * 128 * Tl::kRow + in) >> 4), db + ((piece * ROWS * Tl::kRow + in) >> 4), idesc, k > 0);
   }
 }
-// D[128 x D] (+)= A[128 x ROWS] B, A packed in TMEM (8 columns per 16 rows of B), B a tile of ROWS rows.
-template <int D, int ROWS>
+// D[128 x D] (+)= A[128 x ROWS] B, A packed in TMEM (8 columns per 16 rows of B), B ROWS rows of a tile of TILE.
+template <int D, int ROWS, int TILE = ROWS>
 __device__ __forceinline__ void mma_acc(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_addr, uint32_t idesc, bool first) {
-  const uint64_t db = tile_desc<D>(b_addr, ROWS * TileOf<D>::kRow);
+  const uint64_t db = tile_desc<D>(b_addr, TILE * TileOf<D>::kRow);
 #pragma unroll
   for (int k = 0; k < ROWS / 16; ++k)
     umma_ts(d_tmem, a_tmem + 8 * k, db + (uint64_t)(k * TileOf<D>::kRow), idesc, (first && k == 0) ? 0u : 1u);

@@ -12,16 +12,17 @@
 // atomics, the same result for the same call.
 //
 // Per tile: X = F1 M1^T and Y = F2 M2^T into TMEM (fp32; queries fixed: F = q,
-// dO and M = k, v; keys fixed: F = k, v and M = q, dO), four warps (TMEM lane =
-// fixed row) form P and dS and write them back as 16-bit operands over the
-// scores, then the sums += dS M1 (and P M2) as TS MMAs. D = 32 and 64: one such
-// group of warps, two CTAs per SM; D = 128: two groups on alternating tiles with
-// a score buffer each, one CTA per SM (the sums take 256 TMEM columns).
+// dO and M = k, v; keys fixed: F = k, v and M = q, dO), eight warps (TMEM lane =
+// fixed row, four warps per half of the columns) form P and dS and write them
+// back as 16-bit operands over the scores, then the sums += dS M1 (and P M2) as
+// TS MMAs. D = 32 and 64: one such group of warps, two CTAs per SM; D = 128: two
+// groups on alternating tiles with a score buffer each, one CTA per SM (the sums
+// take 256 TMEM columns).
 //
 // The table's gradient sums dS along diagonals (the bias is one line per tile,
 // see BiasLine). A tile of one bucket adds its rows' sums. In the others a
 // warp passes partial sums from lane to lane: after column c, lane 31 holds the
-// finished sum of diagonal c - 31; the 95 diagonals of its 32 rows then go to
+// finished sum of diagonal c - 31; the 63 diagonals of its 32 x 32 part then go to
 // the warp's bins, equal buckets combined in lane order.
 #include "bias_attention.cuh"
 
@@ -33,10 +34,11 @@ constexpr int kLineN = 127 + kBn;   // offsets in a tile
 
 template <int D, bool kKeys>
 struct BwdCfg {
-  static constexpr int G = D == 128 ? 2 : 1;  // groups of four warps
+  static constexpr int G = D == 128 ? 2 : 1;  // groups of eight warps
   static constexpr int CTAS = D == 128 ? 1 : 2;
   static constexpr int ST = 3;  // stages of the moving tiles
-  static constexpr int THREADS = 32 * (4 * G + 3);
+  static constexpr int kWarps = 8 * G;
+  static constexpr int THREADS = 32 * (kWarps + 3);
   using Line = BiasLine<kLineN, !kKeys>;
   static constexpr int kFixed = 128 * D * 2, kMoving = kBn * D * 2;
   static constexpr int OFF_F = 0;                                   // F1, F2
@@ -44,8 +46,8 @@ struct BwdCfg {
   static constexpr int OFF_LINE = OFF_M + ST * 2 * kMoving;
   static constexpr int OFF_COL = OFF_LINE + (ST * (int)sizeof(Line) + 15) / 16 * 16;  // per stage and column (-lse, -D)
   static constexpr int OFF_DIAG = OFF_COL + (kKeys ? ST * kBn * 8 : 0);
-  static constexpr int OFF_BAR = OFF_DIAG + (kKeys ? 0 : 4 * G * 96 * 4);
-  static constexpr int OFF_BINS = OFF_BAR + 192;                    // [4 G][buckets], queries fixed
+  static constexpr int OFF_BAR = OFF_DIAG + (kKeys ? 0 : kWarps * 64 * 4);
+  static constexpr int OFF_BINS = OFF_BAR + 192;                    // [kWarps][buckets], queries fixed
   static constexpr uint32_t kTmem = D == 128 ? 512 : 256;
   static constexpr int kColAcc = 128 * G;  // sums behind the score buffers
   static_assert(kColAcc + (kKeys ? 2 : 1) * D <= (int)kTmem, "TMEM columns of a CTA");
@@ -58,13 +60,20 @@ struct BwdArgs {
   float* dtab;     // [hq][B * query tiles][buckets] shares of the table's gradient
 };
 
+// D[128 x D] (+)= A[128 x 64] B, A packed in TMEM in two halves of 32 rows of B, 32 columns apart.
+template <int D>
+__device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_addr, uint32_t idesc, bool first) {
+  mma_acc<D, 32, kBn>(d_tmem, a_tmem, b_addr, idesc, first);
+  mma_acc<D, 32, kBn>(d_tmem, a_tmem + 32, b_addr + 32 * TileOf<D>::kRow, idesc, false);
+}
+
 template <class T, int D, bool kKeys>
 __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::CTAS)
     attn_bwd_kernel(const __grid_constant__ BwdArgs args) {
   using C = BwdCfg<D, kKeys>;
   using Line = typename C::Line;
   constexpr int G = C::G, ST = C::ST;
-  constexpr int kMmaWarp = 4 * G;
+  constexpr int kMmaWarp = C::kWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   const BiasAttnArgs& a = args.a;
   Line* lines = reinterpret_cast<Line*>(smem + C::OFF_LINE);
@@ -103,11 +112,11 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
   if (tid == 0) {
     for (int k = 0; k < ST; ++k) {
       mbar_init(&full[k], 3);
-      mbar_init(&free_[k], 1 + 4);
+      mbar_init(&free_[k], 1 + 8);
     }
     for (int k = 0; k < G; ++k) {
       mbar_init(&s_full[k], 1);
-      mbar_init(&ds_full[k], 4);
+      mbar_init(&ds_full[k], 8);
     }
     mbar_init(f_full, 2);
     mbar_init(done, 1);
@@ -176,49 +185,55 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     // ------------------------------------------------------------ MMA issue
     // (the whole warp waits, one elected lane issues)
     constexpr uint32_t id_s = idesc16<T>(128, kBn, 0, 0), id_acc = idesc16<T>(128, D, 0, 1);
-    int ss = 0;  // stage and parity of the next scores' tile
-    uint32_t sp = 0;
-    auto scores = [&](int t) {
-      if (!warp_wait(&full[ss], sp, a.ctx, kErrAttnMma)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t buf = tmem + 128 * (t % G), m1 = sm + ss * 2 * C::kMoving;
-        mma_rows<D, kBn>(buf, sf, m1, id_s);
-        mma_rows<D, kBn>(buf + 64, sf + C::kFixed, m1 + C::kMoving, id_s);
-        umma_commit(&s_full[t % G]);
-      }
-      __syncwarp();
-      if (++ss == ST) ss = 0, sp ^= 1;
-      return true;
+    auto scores = [&](int t) {  // by the elected lane
+      const uint32_t buf = tmem + 128 * (t % G), m1 = sm + t % ST * 2 * C::kMoving;
+      mma_rows<D, kBn>(buf, sf, m1, id_s);
+      mma_rows<D, kBn>(buf + 64, sf + C::kFixed, m1 + C::kMoving, id_s);
+      umma_commit(&s_full[t % G]);
     };
+    auto wait_tile = [&](int t) { return warp_wait(&full[t % ST], (t / ST) & 1, a.ctx, kErrAttnMma); };
     bool ok = nt > 0 && warp_wait(f_full, 0, a.ctx, kErrAttnMma);
-    for (int t = 0; t < G && t < nt && ok; ++t) ok = scores(t);
-    int as = 0;
-    for (int t = 0; t < nt && ok; ++t) {
-      ok = warp_wait(&ds_full[t % G], (t / G) & 1, a.ctx, kErrAttnMma);
+    for (int t = 0; t < G && t < nt && ok; ++t) {
+      ok = wait_tile(t);
       if (!ok) break;
       tc_fence_after();
+      if (elect_one()) scores(t);
+      __syncwarp();
+    }
+    for (int t = 0; t < nt && ok; ++t) {
+      const int u = t + G;  // the tile whose scores take this one's buffer
+      ok = warp_wait(&ds_full[t % G], (t / G) & 1, a.ctx, kErrAttnMma);
+      if (!ok) break;
+      // the scores that follow go out at once when their tiles are there
+      const bool now = u < nt && __all_sync(0xffffffffu, mbar_test(&full[u % ST], (u / ST) & 1));
+      tc_fence_after();
       if (elect_one()) {
-        const uint32_t buf = tmem + 128 * (t % G), m1 = sm + as * 2 * C::kMoving;
-        mma_acc<D, kBn>(tmem + C::kColAcc, buf + 64, m1, id_acc, t == 0);  // dq += dS k, or dk += dS^T q
-        if (kKeys) mma_acc<D, kBn>(tmem + C::kColAcc + D, buf, m1 + C::kMoving, id_acc, t == 0);  // dv += P^T dO
-        umma_commit(&free_[as]);
+        const uint32_t buf = tmem + 128 * (t % G), m1 = sm + t % ST * 2 * C::kMoving;
+        mma_halves<D>(tmem + C::kColAcc, buf + 64, m1, id_acc, t == 0);  // dq += dS k, or dk += dS^T q
+        if (kKeys) mma_halves<D>(tmem + C::kColAcc + D, buf, m1 + C::kMoving, id_acc, t == 0);  // dv += P^T dO
+        umma_commit(&free_[t % ST]);
         if (t == nt - 1) umma_commit(done);
+        if (now) scores(u);  // runs after the sums, which read these columns
       }
       __syncwarp();
-      if (++as == ST) as = 0;
-      if (t + G < nt) ok = scores(t + G);  // runs after the sums, which read these columns
+      if (u < nt && !now) {
+        ok = wait_tile(u);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) scores(u);
+        __syncwarp();
+      }
     }
   } else {
     // ------------------------------------------------------------ P and dS
-    const int g = warp >> 2;
+    const int quad = warp >> 2, g = quad >> 1, c_first = 32 * (quad & 1);  // group, first column of its half of a tile
     const int row = (warp & 3) * 32 + lane, i = f0 + row;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t buf = tmem + tl + 128 * g;
     const float c = a.scale * kLog2E;
     const float2 c2 = make_float2(c, c);
     float* bins = reinterpret_cast<float*>(smem + C::OFF_BINS) + warp * a.buckets;
-    float* diag = reinterpret_cast<float*>(smem + C::OFF_DIAG) + warp * 96;
+    float* diag = reinterpret_cast<float*>(smem + C::OFF_DIAG) + warp * 64;
     float nl = -INFINITY, nd = 0.f;  // queries fixed: -lse (log2) and -D of the row
     float flat_sum = 0.f;            // dS of tiles of one bucket, until the bucket changes
     int flat_bucket = 0;
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
             nd = -dd;
           }
         }
-        if (g == 0) args.delta[r] = dd;
+        if (quad == 0) args.delta[r] = dd;
       }
       __syncwarp();
     }
@@ -275,55 +290,71 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
         flush_flat();
         flat_bucket = bl.which;
       }
+      // this warp's half of the tile, of one bucket or not, with keys missing or not
+      auto form = [&](auto flat_, auto cut_) {
+        constexpr bool kFlat = decltype(flat_)::value, kCut = decltype(cut_)::value;
 #pragma unroll
-      for (int c0 = 0; c0 < kBn; c0 += 32) {
-        uint32_t us[32], ud[32], w[16];
-        tmem_ld32(buf + c0, us);
-        tmem_ld32(buf + 64 + c0, ud);
-        tmem_wait_ld_keep(us);
-        tmem_wait_ld_keep(ud);
-        float ds[32];
+        for (int e = 0; e < 32; e += 16) {
+          const int c0 = c_first + e;
+          uint32_t us[16], ud[16], w[8], wp[8];
+          tmem_ld16(buf + c0, us);
+          tmem_ld16(buf + 64 + c0, ud);
+          tmem_wait_ld_keep(us);
+          tmem_wait_ld_keep(ud);
+          float ds[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float2 off, d2;
-          if (kKeys) {
-            const float4 q = *reinterpret_cast<const float4*>(col + c0 + k);  // two columns' (-lse, -D)
-            off = make_float2(q.x, q.z);
-            d2 = make_float2(q.y, q.w);
-          } else {
-            off = make_float2(nl, nl);
-            d2 = make_float2(nd, nd);
+          for (int k = 0; k < 16; k += 2) {
+            float2 off = make_float2(nl, nl), d2 = make_float2(nd, nd);
+            if (kKeys) {
+              const float4 q = *reinterpret_cast<const float4*>(col + c0 + k);  // two columns' (-lse, -D)
+              off = make_float2(q.x, q.z);
+              d2 = make_float2(q.y, q.w);
+            }
+            if (kFlat)
+              off = __fadd2_rn(off, make_float2(value, value));
+            else if (kKeys)
+              off = __fadd2_rn(off, make_float2(line[-(c0 + k)], line[-(c0 + k + 1)]));
+            else
+              off = __fadd2_rn(off, make_float2(line[c0 + k], line[c0 + k + 1]));
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(us[k]), __uint_as_float(us[k + 1])), c2, off);
+            if (kCut) {
+              x.x = c0 + k < live ? x.x : -INFINITY;
+              x.y = c0 + k + 1 < live ? x.y : -INFINITY;
+            }
+            const float2 pr = make_float2(ex2(x.x), ex2(x.y));
+            const float2 d =
+                __fmul2_rn(pr, __fadd2_rn(make_float2(__uint_as_float(ud[k]), __uint_as_float(ud[k + 1])), d2));
+            if (kKeys) wp[k / 2] = pack2<T>(pr.x, pr.y);
+            w[k / 2] = pack2<T>(d.x, d.y);
+            ds[k] = d.x;
+            ds[k + 1] = d.y;
+            if (!kKeys && kFlat) sum = __fadd2_rn(sum, d);
           }
-          if (flat)
-            off = __fadd2_rn(off, make_float2(value, value));
-          else if (kKeys)
-            off = __fadd2_rn(off, make_float2(line[-(c0 + k)], line[-(c0 + k + 1)]));
-          else
-            off = __fadd2_rn(off, make_float2(line[c0 + k], line[c0 + k + 1]));
-          float2 x = __ffma2_rn(make_float2(__uint_as_float(us[k]), __uint_as_float(us[k + 1])), c2, off);
-          if (!kKeys && live < kBn) {
-            x.x = c0 + k < live ? x.x : -INFINITY;
-            x.y = c0 + k + 1 < live ? x.y : -INFINITY;
+          // over scores of this half that have been read
+          if (kKeys) tmem_st8(buf + c_first + e / 2, wp);
+          tmem_st8(buf + 64 + c_first + e / 2, w);
+          if (!kKeys && !kFlat) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float up = __shfl_up_sync(0xffffffffu, acc, 1);
+              acc = (lane == 0 ? 0.f : up) + ds[k];
+              if (lane == 31) diag[e + k] = acc;
+            }
           }
-          const float2 pr = make_float2(ex2(x.x), ex2(x.y));
-          const float2 e =
-              __fmul2_rn(pr, __fadd2_rn(make_float2(__uint_as_float(ud[k]), __uint_as_float(ud[k + 1])), d2));
-          if (kKeys) us[k / 2] = pack2<T>(pr.x, pr.y);
-          w[k / 2] = pack2<T>(e.x, e.y);
-          ds[k] = e.x;
-          ds[k + 1] = e.y;
-          if (!kKeys && flat) sum = __fadd2_rn(sum, e);
         }
-        if (kKeys) tmem_st16(buf + c0 / 2, us);
-        tmem_st16(buf + 64 + c0 / 2, w);
-        if (!kKeys && !flat) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float up = __shfl_up_sync(0xffffffffu, acc, 1);
-            acc = (lane == 0 ? 0.f : up) + ds[k];
-            if (lane == 31) diag[c0 + k] = acc;
-          }
-        }
+      };
+      using Yes = std::true_type;
+      using No = std::false_type;
+      if (live >= kBn) {
+        if (flat)
+          form(Yes{}, No{});
+        else
+          form(No{}, No{});
+      } else if constexpr (!kKeys) {
+        if (flat)
+          form(Yes{}, Yes{});
+        else
+          form(No{}, Yes{});
       }
       tmem_wait_st();
       tc_fence_before();
@@ -333,14 +364,14 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
         if (flat) {
           flat_sum += sum.x + sum.y;
         } else {
-          if (lane < 31) diag[kBn - 1 + 31 - lane] = acc;
+          if (lane < 31) diag[62 - lane] = acc;
           __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const int at = lane + 32 * k;  // diagonal at - 31
-            const bool have = at < kBn + 31;
+          for (int k = 0; k < 2; ++k) {
+            const int at = lane + 32 * k;  // diagonal at - 31 of the warp's 32 x 32
+            const bool have = at < 63;
             float v = have ? diag[at] : 0.f;
-            const int bucket = have ? bl.bucket[at + 96 - 32 * (warp & 3)] : -1;
+            const int bucket = have ? bl.bucket[at + 96 + c_first - 32 * (warp & 3)] : -1;
             // a run of one bucket adds up into its last lane
             const int before = __shfl_up_sync(0xffffffffu, bucket, 1);
             const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 || before != bucket);
@@ -376,36 +407,31 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     if (ok && nt > 0) ok = warp_wait(done, 0, a.ctx, kErrAttnSoftmax);
     tc_fence_after();
     if (ok) {
-      // queries fixed: group g writes its part of dq's channels; keys fixed: dk and dv, one group each when there are two
+      // every quad writes its part of the sums' columns: dq, or dk and then dv
       const int n_out = kKeys ? a.Lk : a.Lq;
       const bool some = i < (kKeys ? sl.nk : sl.nq) && nt > 0;
-      constexpr int kOuts = kKeys && G == 1 ? 2 : 1;
-      constexpr int kCols = !kKeys && G == 2 ? D / 2 : D;
+      constexpr int kCols = (kKeys ? 2 : 1) * D / (2 * G);
+      const int first = quad * kCols;
+      const bool is_dv = kKeys && first >= D;
+      const Heads& out = !kKeys ? a.dq : (is_dv ? a.dv : a.dk);
+      const float scale = is_dv ? 1.f : a.scale;
+      T* dst = static_cast<T*>(out.p) + (i < n_out ? out.at(b, i, hf) : 0) + (is_dv ? first - D : first);
 #pragma unroll
-      for (int o = 0; o < kOuts; ++o) {
-        const int which = kOuts == 2 ? o : g;  // keys fixed: 0 dk, 1 dv
-        const Heads& out = !kKeys ? a.dq : (which == 0 ? a.dk : a.dv);
-        const float scale = kKeys && which == 1 ? 1.f : a.scale;
-        const int first = !kKeys && G == 2 ? g * kCols : 0;
-        const uint32_t from = tmem + tl + C::kColAcc + (kKeys ? which * D : 0) + first;
-        T* dst = static_cast<T*>(out.p) + (i < n_out ? out.at(b, i, hf) : 0) + first;
+      for (int c0 = 0; c0 < kCols; c0 += 16) {
+        uint32_t u[16];
+        if (nt > 0) {
+          tmem_ld16(tmem + tl + C::kColAcc + first + c0, u);
+          tmem_wait_ld_keep(u);
+        }
+        float f[16];
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 16) {
-          uint32_t u[16];
-          if (nt > 0) {
-            tmem_ld16(from + c0, u);
-            tmem_wait_ld_keep(u);
-          }
-          float f[16];
+        for (int k = 0; k < 16; ++k) f[k] = some ? __uint_as_float(u[k]) * scale : 0.f;
+        if (i < n_out) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] = some ? __uint_as_float(u[k]) * scale : 0.f;
-          if (i < n_out) {
-#pragma unroll
-            for (int k = 0; k < 16; k += 8)
-              *reinterpret_cast<uint4*>(dst + c0 + k) =
-                  make_uint4(pack2<T>(f[k], f[k + 1]), pack2<T>(f[k + 2], f[k + 3]), pack2<T>(f[k + 4], f[k + 5]),
-                             pack2<T>(f[k + 6], f[k + 7]));
-          }
+          for (int k = 0; k < 16; k += 8)
+            *reinterpret_cast<uint4*>(dst + c0 + k) =
+                make_uint4(pack2<T>(f[k], f[k + 1]), pack2<T>(f[k + 2], f[k + 3]), pack2<T>(f[k + 4], f[k + 5]),
+                           pack2<T>(f[k + 6], f[k + 7]));
         }
       }
     }
@@ -421,7 +447,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     float* out = args.dtab + (((long long)hf * a.B + b) * fixed_tiles + f0 / 128) * a.buckets;
     for (int k = tid; k < a.buckets; k += C::THREADS) {
       float v = 0.f;
-      for (int w = 0; w < 4 * G; ++w) v += bins[w * a.buckets + k];
+      for (int w = 0; w < C::kWarps; ++w) v += bins[w * a.buckets + k];
       out[k] = v;
     }
   }
@@ -449,8 +475,8 @@ template <class T, int D, bool kKeys>
 cudaError_t pass(BwdArgs& args, cudaStream_t st) {
   using C = BwdCfg<D, kKeys>;
   const BiasAttnArgs& a = args.a;
-  const int smem = C::OFF_BINS + (kKeys ? 0 : 4 * C::G * a.buckets * 4);
-  constexpr int kMost = C::OFF_BINS + (kKeys ? 0 : 4 * C::G * kMaxBuckets * 4);
+  const int smem = C::OFF_BINS + (kKeys ? 0 : C::kWarps * a.buckets * 4);
+  constexpr int kMost = C::OFF_BINS + (kKeys ? 0 : C::kWarps * kMaxBuckets * 4);
   static_assert(C::CTAS * (kMost + 1024) <= 228 * 1024, "shared memory of an SM");
   cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<T, D, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   if (e != cudaSuccess) return e;

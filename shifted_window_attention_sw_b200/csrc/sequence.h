@@ -52,7 +52,7 @@ cudaError_t launch_qk_norm_forward(const QkNormArgs& a, int dtype, cudaStream_t 
 size_t qk_norm_scratch_bytes(const QkNormArgs& a, int dtype);
 cudaError_t launch_qk_norm_backward(const QkNormArgs& a, int dtype, void* scratch, cudaStream_t st);
 
-constexpr int kMaxBuckets = 1024;
+constexpr int kMaxBuckets = 512;
 
 struct BiasAttnArgs {
   int B, Lq, Lk, hq, hk, d;

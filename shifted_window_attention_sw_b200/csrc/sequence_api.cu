@@ -165,8 +165,8 @@ int check_bias_attention(int dtype, int B, int Lq, int Lk, int hq, int hk, int d
   if (!aligned(bias->table, 2) || !aligned(bias->map, 4))
     return fail(VSWIN_ERR_INVALID_ARG, "bias table or map is misaligned");
   if (bias->buckets <= 0 || bias->buckets > kMaxBuckets || bias->max_distance < 0 || bias->max_distance > (1 << 20))
-    return fail(VSWIN_ERR_INVALID_ARG, "buckets %d must lie in [1, 1024] and max_distance %d in [0, 2^20]",
-                bias->buckets, bias->max_distance);
+    return fail(VSWIN_ERR_INVALID_ARG, "buckets %d must lie in [1, %d] and max_distance %d in [0, 2^20]",
+                bias->buckets, kMaxBuckets, bias->max_distance);
   a->table = bias->table, a->map = bias->map, a->buckets = bias->buckets, a->D = bias->max_distance;
   if (vis) {
     if (!aligned(vis->q_lens, 4) || !aligned(vis->kv_lens, 4) || !aligned(vis->q_start, 4))
