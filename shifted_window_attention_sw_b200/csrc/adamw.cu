@@ -12,7 +12,7 @@
 // least 1, so that it never reads back as zero under the square root.
 //
 // Bound by HBM: each state is read and written once. A tensor is cut into
-// chunks of kChunk elements; the blocks walk the chunks of all tensors (whose
+// chunks; the blocks walk the chunks of all tensors (whose
 // records travel as the kernel's parameter, so that nothing is uploaded and the
 // step can be captured), eight elements per thread. With 8-bit moments a warp
 // holds one block of 256 and finds its scale by shuffles.
@@ -24,13 +24,14 @@ namespace vswin {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = kThreads * 8;
+constexpr int kRun = kThreads * 8;  // elements of a block's run
 
 template <int kCap>
 struct Table {
   AdamwTensor t[kCap];
   long long first[kCap + 1];  // chunks before tensor i
   int count;
+  int chunk;                  // elements of a chunk: one run, or two when there are chunks for every block
 };
 
 // Eight elements from index i of n; elements past n read as zero.
@@ -126,22 +127,24 @@ __device__ __forceinline__ void store_codes(void* p, bool vec, long long i, long
 // Byte k of w as a float, and back: 2^23 + n has n in its low bits, so a byte
 // permutation and one addition convert (the conversion instructions run at a
 // quarter of the rate).
-__device__ __forceinline__ float byte_float(uint32_t w, int k) {
-  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + k)) - 8388608.f;
+__device__ __forceinline__ float byte_bits(uint32_t w, int k) {  // 2^23 + byte
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + k));
 }
 __device__ __forceinline__ uint32_t round_byte(float x) { return __float_as_uint(x + 12582912.f); }  // low byte: rint(x)
 __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
-// Signed codes come as bytes with the sign bit flipped (code + 128).
+// Values of codes, with s / 127^2 and s / 255^4 for s. Signed codes come as bytes
+// with the sign bit flipped (code + 128).
+constexpr float kUnitM = 1.f / (127.f * 127.f), kUnitV = 1.f / (255.f * 255.f * 255.f * 255.f);
 __device__ __forceinline__ float decode_m(uint32_t w, int k, float s) {
-  const float x = (byte_float(w, k) - 128.f) * (1.f / 127.f);
-  return s * x * fabsf(x);
+  const float c = byte_bits(w, k) - 8388736.f;
+  return s * (c * fabsf(c));
 }
 __device__ __forceinline__ float decode_v(uint32_t w, int k, float s) {
-  const float x = byte_float(w, k) * (1.f / 255.f);
-  const float x2 = x * x;
-  return s * (x2 * x2);
+  const float c = byte_bits(w, k) - 8388608.f;
+  const float c2 = c * c;
+  return s * (c2 * c2);
 }
 constexpr uint32_t kFlip = 0x80808080u;
 
@@ -191,68 +194,78 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   }
   const float gs = h.grad_scale ? *h.grad_scale : 1.f;
   const int lane = threadIdx.x & 31;
+  int at = 0;  // tensor of the chunk: chunks only go up
   for (long long chunk = blockIdx.x; chunk < tab.first[tab.count]; chunk += gridDim.x) {
-    int lo = 0, hi = tab.count - 1;  // the tensor of this chunk
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (tab.first[mid] <= chunk)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const AdamwTensor& t = tab.t[lo];
-    const long long n = t.n, i = (chunk - tab.first[lo]) * kChunk + threadIdx.x * 8;
-    if (kBits == 32 && i >= n) continue;
-    if (kBits == 8 && i - lane * 8 >= n) continue;  // a whole warp's block lies behind the tensor
-    const bool vec = t.vec != 0;
-    float p[8], g[8], m[8], v[8];
-    load_elems(t.master ? (const void*)t.master : t.p, t.master ? kF32 : t.p_type, vec, i, n, p);
-    load_elems(t.g, t.g_type, vec, i, n, g);
-    if (kBits == 32) {
-      load_elems(t.m, kF32, vec, i, n, m);
-      load_elems(t.v, kF32, vec, i, n, v);
-    } else {
-      const uint2 cm = load_codes(t.m, vec, i, n), cv = load_codes(t.v, vec, i, n);
-      const float sm = t.ms[i / kAdamwBlock], sv = t.vs[i / kAdamwBlock];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] = decode_m((k < 4 ? cm.x : cm.y) ^ kFlip, k & 3, sm);
-        v[k] = decode_v(k < 4 ? cv.x : cv.y, k & 3, sv);
+    if (chunk >= tab.first[at + 1]) {
+      int hi = tab.count - 1;
+      while (at < hi) {
+        const int mid = (at + hi + 1) / 2;
+        if (tab.first[mid] <= chunk)
+          at = mid;
+        else
+          hi = mid - 1;
       }
     }
-    float root[8];  // sqrt(v)
+    const AdamwTensor& t = tab.t[at];
+    const long long n = t.n, start = (chunk - tab.first[at]) * tab.chunk + threadIdx.x * 8;
+    for (long long i = start; i < start + tab.chunk; i += kRun) {
+      if (kBits == 32 && i >= n) break;
+      if (kBits == 8 && i - lane * 8 >= n) break;  // a whole warp's block lies behind the tensor
+      const bool vec = t.vec != 0;
+      float p[8], g[8], m[8], v[8];
+      load_elems(t.master ? (const void*)t.master : t.p, t.master ? kF32 : t.p_type, vec, i, n, p);
+      load_elems(t.g, t.g_type, vec, i, n, g);
+      if (kBits == 32) {
+        load_elems(t.m, kF32, vec, i, n, m);
+        load_elems(t.v, kF32, vec, i, n, v);
+      } else {
+        const uint2 cm = load_codes(t.m, vec, i, n), cv = load_codes(t.v, vec, i, n);
+        const float sm = t.ms[i / kAdamwBlock] * kUnitM, sv = t.vs[i / kAdamwBlock] * kUnitV;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float gr = g[k] * gs;
-      m[k] = h.b1 * m[k] + h.c1 * gr;
-      v[k] = h.b2 * v[k] + h.c2 * (gr * gr);
-      root[k] = sqrt_fast(v[k]);
-      p[k] = t.keep * p[k] - step_size * m[k] * rcp_fast(root[k] * inv_bc2 + h.eps);
-    }
-    if (t.master) store_elems(t.master, kF32, vec, i, n, p);
-    store_elems(t.p, t.p_type, vec, i, n, p);
-    if (kBits == 32) {
-      store_elems(t.m, kF32, vec, i, n, m);
-      store_elems(t.v, kF32, vec, i, n, v);
-    } else {
-      // (elements behind the tensor are zero here)
-      const float sm = warp_max_nan(max3_nan(max3_nan(m[0], m[1], m[2]), max3_nan(m[3], m[4], m[5]), max3_nan(m[6], m[7], 0.f)));
-      const float sv = warp_max_nan(max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), max3_nan(v[6], v[7], 0.f)));
-      // code = 127 sqrt(|m| / s), 255 sqrt(sqrt(v) / sqrt(s)); blocks below 2^-100 have no use for codes, and 1 / s no overflow
-      const float im = sm >= 0x1p-100f ? 127.f * 127.f / sm : 0.f;
-      const float iv = sv >= 0x1p-100f ? 255.f * 255.f * rsqrtf(sv) : 0.f;
-      uint32_t cm[8], cv[8];
+        for (int k = 0; k < 8; ++k) {
+          m[k] = decode_m((k < 4 ? cm.x : cm.y) ^ kFlip, k & 3, sm);
+          v[k] = decode_v(k < 4 ? cv.x : cv.y, k & 3, sv);
+        }
+      }
+      float root[8];  // sqrt(v)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float c = sqrt_flush(root[k] * iv);
-        cm[k] = round_byte(copysignf(sqrt_flush(fabsf(m[k]) * im), m[k]));
-        cv[k] = round_byte(v[k] > 0.f ? fmaxf(c, 1.f) : c);
+        const float gr = g[k] * gs;
+        m[k] = h.b1 * m[k] + h.c1 * gr;
+        v[k] = h.b2 * v[k] + (h.c2 * gr) * gr;
+        if (kBits == 32) {
+          root[k] = sqrt_fast(v[k]);
+          p[k] = t.keep * p[k] - (step_size * m[k]) * rcp_fast(root[k] * inv_bc2 + h.eps);
+        } else {  // (8-bit moments do not resolve v below 2^-126: the root may flush)
+          root[k] = sqrt_flush(v[k]);
+          p[k] = t.keep * p[k] - (step_size * m[k]) * rcp_fast(fmaxf(root[k] * inv_bc2 + h.eps, 0x1p-66f));
+        }
       }
-      store_codes(t.m, vec, i, n, make_uint2(pack_bytes(cm[0], cm[1], cm[2], cm[3]), pack_bytes(cm[4], cm[5], cm[6], cm[7])));
-      store_codes(t.v, vec, i, n, make_uint2(pack_bytes(cv[0], cv[1], cv[2], cv[3]), pack_bytes(cv[4], cv[5], cv[6], cv[7])));
-      if (lane == 0) {
-        t.ms[i / kAdamwBlock] = sm;
-        t.vs[i / kAdamwBlock] = sv;
+      if (t.master) store_elems(t.master, kF32, vec, i, n, p);
+      store_elems(t.p, t.p_type, vec, i, n, p);
+      if (kBits == 32) {
+        store_elems(t.m, kF32, vec, i, n, m);
+        store_elems(t.v, kF32, vec, i, n, v);
+      } else {
+        // (elements behind the tensor are zero here)
+        const float sm = warp_max_nan(max3_nan(max3_nan(m[0], m[1], m[2]), max3_nan(m[3], m[4], m[5]), max3_nan(m[6], m[7], 0.f)));
+        const float sv = warp_max_nan(max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), max3_nan(v[6], v[7], 0.f)));
+        // code = 127 sqrt(|m| / s), 255 sqrt(sqrt(v) / sqrt(s)); blocks below 2^-100 have no use for codes, and 1 / s no overflow
+        const float im = sm >= 0x1p-100f ? 127.f * 127.f / sm : 0.f;
+        const float iv = sv >= 0x1p-100f ? 255.f * 255.f * rsqrtf(sv) : 0.f;
+        uint32_t cm[8], cv[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float c = sqrt_flush(root[k] * iv);
+          cm[k] = round_byte(copysignf(sqrt_flush(fabsf(m[k]) * im), m[k]));
+          cv[k] = round_byte(fmaxf(c, v[k] > 0.f ? 1.f : 0.f));
+        }
+        store_codes(t.m, vec, i, n, make_uint2(pack_bytes(cm[0], cm[1], cm[2], cm[3]), pack_bytes(cm[4], cm[5], cm[6], cm[7])));
+        store_codes(t.v, vec, i, n, make_uint2(pack_bytes(cv[0], cv[1], cv[2], cv[3]), pack_bytes(cv[4], cv[5], cv[6], cv[7])));
+        if (lane == 0) {
+          t.ms[i / kAdamwBlock] = sm;
+          t.vs[i / kAdamwBlock] = sv;
+        }
       }
     }
   }
@@ -264,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) adamw_decode_kernel(const int8_t* m,
                                                                const float* vs, long long n, bool vec, void* mo, void* vo) {
   const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * 16;
   if (i >= n) return;
-  const float sm = ms[i / kAdamwBlock], sv = vs[i / kAdamwBlock];
+  const float sm = ms[i / kAdamwBlock] * kUnitM, sv = vs[i / kAdamwBlock] * kUnitV;
   uint4 cm, cv;
   if (vec && i + 16 <= n) {
     cm = *reinterpret_cast<const uint4*>(m + i);
@@ -292,16 +305,19 @@ __global__ void __launch_bounds__(kThreads) adamw_decode_kernel(const int8_t* m,
 template <int kCap>
 cudaError_t launch_cap(const AdamwTensor* t, int count, int bits, const AdamwHyper& h, cudaStream_t st) {
   Table<kCap> tab;
+  const long long cap = (long long)sm_count() * 8;
   long long chunks = 0;
+  for (int i = 0; i < count; ++i) chunks += (t[i].n + kRun - 1) / kRun;
+  tab.chunk = chunks > 2 * cap ? 2 * kRun : kRun;
+  chunks = 0;
   for (int i = 0; i < count; ++i) {
     tab.t[i] = t[i];
     tab.first[i] = chunks;
-    chunks += (t[i].n + kChunk - 1) / kChunk;
+    chunks += (t[i].n + tab.chunk - 1) / tab.chunk;
   }
   tab.first[count] = chunks;
   tab.count = count;
   if (chunks == 0) return cudaSuccess;
-  const long long cap = (long long)sm_count() * 8;
   const int grid = (int)(chunks < cap ? chunks : cap);
   prof_begin(kKindOther, st);
   if (bits == 32)

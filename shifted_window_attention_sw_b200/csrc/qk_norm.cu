@@ -180,90 +180,111 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum_a[k] = sum_b[k] = 0.f;
   }
-  // token first + n * step of the walk is token l of sequence b
-  const long long tokens = (long long)a.B * a.L;
-  const long long first = (long long)block * per;
+  // token n of the walk is token l of sequence b; of its heads, h0 on are next
+  const int tokens = a.B * a.L;  // below 2^31
   const int step = blocks * per, step_b = step / a.L, step_l = step % a.L;
-  int b = (int)((first + g / hpb) / a.L), l = (int)((first + g / hpb) % a.L);
+  int n = block * per + g / hpb, b = n / a.L, l = n % a.L, h0 = 0;
+  int left = tokens - block * per;  // the block's first token is there while this is positive: same for every lane
+  Vec8<T> u0, u1, d0, d1;
+  auto fetch = [&]() {  // a row's pieces, one step ahead of their use (row 0 where there is none)
+    const int h = h0 + g % hpb;
+    const bool on = live && n < tokens && h < heads;
+    const T* xp = static_cast<const T*>(a.x[w].p) + (on ? a.x[w].at(b, l, h) : 0);
+    load8(xp + (on ? c.c0 : 0), u0);
+    load8(xp + (on ? c.c1 : 0), u1);
+    if (kBackward) {
+      const T* yp = static_cast<const T*>(a.y[w].p) + (on ? a.y[w].at(b, l, h) : 0);
+      load8(yp + (on ? c.c0 : 0), d0);
+      load8(yp + (on ? c.c1 : 0), d1);
+    }
+  };
+  if (left > 0) fetch();
   // every lane of a warp makes the same number of turns (the sums below are warp-wide)
-  for (long long n = first; n < tokens; n += step) {
-    const bool here = live && n + g / hpb < tokens;
-    if (here && c.angle >= 0) load_angles(a, c, angle_row(a, b, l), cs, sn);
-    for (int h0 = 0; h0 < heads; h0 += hpb) {
-      const int h = h0 + g % hpb;
-      const bool on = here && h < heads;
-      float xa[8], xb[8], ya[8], yb[8];
+  while (left > 0) {
+    const int bn = b, ln = l, hn = h0 + g % hpb;
+    const bool on = live && n < tokens && hn < heads;
+    if (h0 == 0 && on && c.angle >= 0) load_angles(a, c, angle_row(a, b, l), cs, sn);
+    float xa[8], xb[8], ya[8], yb[8];
+    unpack8(u0, xa);
+    unpack8(u1, xb);
+    to_pairs<kInter>(xa, xb);
+    if (kBackward) {
+      unpack8(d0, ya);
+      unpack8(d1, yb);
+      to_pairs<kInter>(ya, yb);
+    }
+    h0 += hpb;
+    if (h0 >= heads) {
+      h0 = 0;
+      n += step;
+      left -= step;
+      b += step_b;
+      l += step_l;
+      if (l >= a.L) l -= a.L, ++b;
+    }
+    if (left > 0) fetch();
+    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) xa[k] = xb[k] = ya[k] = yb[k] = 0.f;
-      if (on) {
-        const T* xp = static_cast<const T*>(a.x[w].p) + a.x[w].at(b, l, h);
-        Vec8<T> u0, u1, d0, d1;
-        load8(xp + c.c0, u0);
-        load8(xp + c.c1, u1);
-        if (kBackward) {
-          const T* yp = static_cast<const T*>(a.y[w].p) + a.y[w].at(b, l, h);
-          load8(yp + c.c0, d0);
-          load8(yp + c.c1, d1);
-        }
-        unpack8(u0, xa);
-        unpack8(u1, xb);
-        to_pairs<kInter>(xa, xb);
-        if (kBackward) {
-          unpack8(d0, ya);
-          unpack8(d1, yb);
-          to_pairs<kInter>(ya, yb);
-        }
+    for (int k = 0; k < 8; k += 2) {
+      s2 = __ffma2_rn(make_float2(xa[k], xa[k + 1]), make_float2(xa[k], xa[k + 1]), s2);
+      s2 = __ffma2_rn(make_float2(xb[k], xb[k + 1]), make_float2(xb[k], xb[k + 1]), s2);
+    }
+    // lanes behind the row's width hold another row's channels: their share is not taken
+    const float r = rsqrtf(group_sum<G>(t < a.d / 16 ? s2.x + s2.y : 0.f) * inv_d + a.eps);
+    const float2 r2 = make_float2(r, r);
+    if (!kBackward) {
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float2 cc = make_float2(cs[k], cs[k + 1]), ss = make_float2(sn[k], sn[k + 1]);
+        const float2 na = __fmul2_rn(__fmul2_rn(make_float2(xa[k], xa[k + 1]), r2), make_float2(ga[k], ga[k + 1]));
+        const float2 nb = __fmul2_rn(__fmul2_rn(make_float2(xb[k], xb[k + 1]), r2), make_float2(gb[k], gb[k + 1]));
+        const float2 p = __fmul2_rn(nb, ss);
+        const float2 u = __ffma2_rn(na, cc, make_float2(-p.x, -p.y));
+        const float2 v = __ffma2_rn(nb, cc, __fmul2_rn(na, ss));
+        ya[k] = u.x, ya[k + 1] = u.y, yb[k] = v.x, yb[k + 1] = v.y;
       }
-      float ss = 0.f;
+      if (on) {
+        from_pairs<kInter>(ya, yb);
+        T* yp = static_cast<T*>(a.y[w].p) + a.y[w].at(bn, ln, hn);
+        store8(yp + c.c0, ya);
+        store8(yp + c.c1, yb);
+      }
+    } else {
+      float2 along2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(xa[k], xa[k], fmaf(xb[k], xb[k], ss));
-      const float r = rsqrtf(group_sum<G>(ss) * inv_d + a.eps);
-      if (!kBackward) {
+      for (int k = 0; k < 8; k += 2) {
+        const float2 cc = make_float2(cs[k], cs[k + 1]), ss = make_float2(sn[k], sn[k + 1]);
+        const float2 da = make_float2(ya[k], ya[k + 1]), db = make_float2(yb[k], yb[k + 1]);
+        const float2 p = __fmul2_rn(da, ss);
+        const float2 gya = __ffma2_rn(da, cc, __fmul2_rn(db, ss));                   // R^T dy
+        const float2 gyb = __ffma2_rn(db, cc, make_float2(-p.x, -p.y));
+        const float2 ua = __fmul2_rn(make_float2(xa[k], xa[k + 1]), r2), ub = __fmul2_rn(make_float2(xb[k], xb[k + 1]), r2);
         if (on) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float na = xa[k] * r * ga[k], nb = xb[k] * r * gb[k];
-            ya[k] = na * cs[k] - nb * sn[k];
-            yb[k] = nb * cs[k] + na * sn[k];
-          }
-          from_pairs<kInter>(ya, yb);
-          T* yp = static_cast<T*>(a.y[w].p) + a.y[w].at(b, l, h);
-          store8(yp + c.c0, ya);
-          store8(yp + c.c1, yb);
+          const float2 sa = __ffma2_rn(gya, ua, make_float2(sum_a[k], sum_a[k + 1]));
+          const float2 sb = __ffma2_rn(gyb, ub, make_float2(sum_b[k], sum_b[k + 1]));
+          sum_a[k] = sa.x, sum_a[k + 1] = sa.y, sum_b[k] = sb.x, sum_b[k + 1] = sb.y;
         }
-      } else {
-        float along = 0.f;
-        if (on) {
+        const float2 ha = __fmul2_rn(gya, make_float2(ga[k], ga[k + 1])), hb = __fmul2_rn(gyb, make_float2(gb[k], gb[k + 1]));
+        along2 = __ffma2_rn(ha, ua, along2);
+        along2 = __ffma2_rn(hb, ub, along2);
+        xa[k] = ua.x, xa[k + 1] = ua.y, xb[k] = ub.x, xb[k + 1] = ub.y;
+        ya[k] = ha.x, ya[k + 1] = ha.y, yb[k] = hb.x, yb[k + 1] = hb.y;
+      }
+      const float along = group_sum<G>(t < a.d / 16 ? along2.x + along2.y : 0.f) * inv_d;
+      const float2 m2 = make_float2(-along, -along);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float gya = ya[k] * cs[k] + yb[k] * sn[k];  // R^T dy
-            const float gyb = yb[k] * cs[k] - ya[k] * sn[k];
-            xa[k] *= r;
-            xb[k] *= r;
-            sum_a[k] = fmaf(gya, xa[k], sum_a[k]);
-            sum_b[k] = fmaf(gyb, xb[k], sum_b[k]);
-            ya[k] = gya * ga[k];
-            yb[k] = gyb * gb[k];
-            along = fmaf(ya[k], xa[k], fmaf(yb[k], xb[k], along));
-          }
-        }
-        along = group_sum<G>(along) * inv_d;
-        if (on) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            ya[k] = r * (ya[k] - xa[k] * along);
-            yb[k] = r * (yb[k] - xb[k] * along);
-          }
-          from_pairs<kInter>(ya, yb);
-          T* dp = static_cast<T*>(a.dx[w].p) + a.dx[w].at(b, l, h);
-          store8(dp + c.c0, ya);
-          store8(dp + c.c1, yb);
-        }
+      for (int k = 0; k < 8; k += 2) {
+        const float2 u = __fmul2_rn(r2, __ffma2_rn(make_float2(xa[k], xa[k + 1]), m2, make_float2(ya[k], ya[k + 1])));
+        const float2 v = __fmul2_rn(r2, __ffma2_rn(make_float2(xb[k], xb[k + 1]), m2, make_float2(yb[k], yb[k + 1])));
+        ya[k] = u.x, ya[k + 1] = u.y, yb[k] = v.x, yb[k + 1] = v.y;
+      }
+      if (on) {
+        from_pairs<kInter>(ya, yb);
+        T* dp = static_cast<T*>(a.dx[w].p) + a.dx[w].at(bn, ln, hn);
+        store8(dp + c.c0, ya);
+        store8(dp + c.c1, yb);
       }
     }
-    b += step_b;
-    l += step_l;
-    if (l >= a.L) l -= a.L, ++b;
   }
   if (kBackward) {
     // this block's share of dgamma: lanes of the same channels, then warps, in a fixed order
