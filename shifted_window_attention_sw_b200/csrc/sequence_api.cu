@@ -102,6 +102,9 @@ int check_qk_norm(int dtype, int B, int L, int hq, int hk, int d, const vswin_he
     const Heads* in[2] = {&a->x[w], backward ? &a->y[w] : nullptr};
     bool replaces = false;
     for (const Heads* i : in) replaces = replaces || (i && same_view(o, *i));
+    // (slices of one buffer interleave; the other tensor's view must not be this one)
+    if (replaces && (o.p == a->x[1 - w].p || (backward && o.p == a->y[1 - w].p)))
+      return fail(VSWIN_ERR_INVALID_ARG, "%s replaces a view that both q and k read", on);
     for (int u = 0; u < 2 && !replaces; ++u)
       if (views_overlap(o, ext[w], a->x[u], ext[u], es) || (backward && views_overlap(o, ext[w], a->y[u], ext[u], es)))
         return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps an input without being the same view", on);
@@ -143,10 +146,10 @@ int check_bias_attention(int dtype, int B, int Lq, int Lk, int hq, int hk, int d
   if (d != 32 && d != 64 && d != 128)
     return fail(VSWIN_ERR_UNSUPPORTED, "attention needs head width 32, 64 or 128 (got %d)", d);
   if (Lq > (1 << 28) || Lk > (1 << 28)) return fail(VSWIN_ERR_UNSUPPORTED, "sequence longer than 2^28");
-  if (hq > 4096 || B > (1 << 20) || (long long)B * hq * ((Lq + 127) / 128) > (1LL << 31) - 1 ||
+  if (hq > 4096 || (long long)B * hq > (1LL << 28) || (long long)B * hq * ((Lq + 127) / 128) > (1LL << 31) - 1 ||
       (long long)B * hk * ((Lk + 127) / 128) > (1LL << 31) - 1)
     return fail(VSWIN_ERR_UNSUPPORTED, "B * heads * length too large");
-  if (!std::isfinite(scale)) return fail(VSWIN_ERR_INVALID_ARG, "scale must be finite");
+  if (!(std::fabs(scale) <= 1e30f)) return fail(VSWIN_ERR_INVALID_ARG, "scale must be finite, at most 1e30 (got %g)", (double)scale);
   *a = BiasAttnArgs{};
   a->B = B, a->Lq = Lq, a->Lk = Lk, a->hq = hq, a->hk = hk, a->d = d;
   a->scale = scale;
@@ -349,7 +352,11 @@ int vswin_adamw_step(const vswin_adamw_tensor* tensors, int count, int bits, dou
   if (!aligned(step_device, 4) || !aligned(grad_scale, 4))
     return fail(VSWIN_ERR_INVALID_ARG, "step_device or grad_scale is not 4-byte aligned");
   std::vector<AdamwTensor> list;
-  list.reserve(count);
+  try {
+    list.reserve(count);
+  } catch (...) {
+    return fail(VSWIN_ERR_NO_MEMORY, "no host memory for a list of %d tensors", count);
+  }
   for (int i = 0; i < count; ++i) {
     const vswin_adamw_tensor& t = tensors[i];
     if (t.n < 0 || t.n > (1LL << 40)) return fail(VSWIN_ERR_INVALID_ARG, "tensor %d: n=%lld", i, t.n);

@@ -424,7 +424,9 @@ def wmsa_forward_host(x_host, window, shift, Wqkv, bqkv, Wproj, bproj, table, he
 
 # ------------------------------------------------------------------ token sequences
 def _refuse(name, t, shape, dtype, device):
-    """Say what is wrong with a tensor that is not of this shape and type on this CUDA device."""
+    """Say what is wrong with a tensor that is not of this shape and type on this CUDA device. ``name`` is a text,
+    or a list's name and an index in it."""
+    name = name if isinstance(name, str) else f"{name[0]}[{name[1]}]"
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -635,17 +637,21 @@ class AdamW:
         self.master = None if not master else self._list("master", master)
         self._records = (_AdamwTensor * len(self.params))()
         for i, (p, r) in enumerate(zip(self.params, self._records)):
-            if p.dtype not in DTYPES:
+            dt, shape, n = DTYPES.get(p.dtype), p.shape, p.numel()
+            if dt is None:
                 raise TypeError(f"params[{i}] must be one of {list(DTYPES)}, got {p.dtype}")
-            r.param = _flat(f"params[{i}]", p, full(p), p.dtype, dev)
-            r.m = _flat(f"m[{i}]", self.m[i], full(p), mt, dev)
-            r.v = _flat(f"v[{i}]", self.v[i], full(p), vt, dev)
+            r.param = _flat(("params", i), p, shape, p.dtype, dev)
+            r.m = _flat(("m", i), self.m[i], shape, mt, dev)
+            r.v = _flat(("v", i), self.v[i], shape, vt, dev)
             if bits == 8:
-                r.m_scale = _flat(f"m_scale[{i}]", self.m_scale[i], blocks(p), torch.float32, dev)
-                r.v_scale = _flat(f"v_scale[{i}]", self.v_scale[i], blocks(p), torch.float32, dev)
+                blocks_of = (-(-n // ADAMW_BLOCK),)
+                r.m_scale = _flat(("m_scale", i), self.m_scale[i], blocks_of, torch.float32, dev)
+                r.v_scale = _flat(("v_scale", i), self.v_scale[i], blocks_of, torch.float32, dev)
             if self.master:
-                r.master = _flat(f"master[{i}]", self.master[i], full(p), torch.float32, dev)
-            r.n, r.weight_decay, r.param_dtype = p.numel(), decay[i], DTYPES[p.dtype]
+                r.master = _flat(("master", i), self.master[i], shape, torch.float32, dev)
+            r.n, r.weight_decay, r.param_dtype = n, decay[i], dt
+        if len({r.param for r in self._records if r.n}) < sum(1 for r in self._records if r.n):
+            raise ValueError("a weight stands in params twice")
         self._shapes = [p.shape for p in self.params]
 
     def _list(self, name, tensors):

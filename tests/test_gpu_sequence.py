@@ -239,6 +239,22 @@ def test_attention_layouts(layout, dtype):
         assert torch.equal(buf, torch.cat((dq, dk, dv), 2))
 
 
+@pytest.mark.parametrize("dim", [0, 1, 2])
+@pytest.mark.parametrize("Lq", [150, 1])
+def test_attention_broadcast_inputs(dim, Lq):
+    # k and v with stride 0 over the batch, the tokens or the heads; q over the batch
+    ins, do = _attn_inputs(BF16, 3, Lq, 150, 4, 4, 64)
+    wide = [t.clone() for t in ins]
+    for n in (1, 2):
+        narrow = ins[n].select(dim, 0).unsqueeze(dim)
+        ins[n] = narrow.expand(3, 150, 4, 64)
+        wide[n] = ins[n].contiguous()
+    ins[0], wide[0] = ins[0][:1].expand(3, -1, -1, -1), ins[0][:1].expand(3, -1, -1, -1).contiguous()
+    got = _attn_check(ins, _map(), do, kv_lens=_i32(150, 77, 3))
+    want = _attn_check(wide, _map(), do, kv_lens=_i32(150, 77, 3))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("dtype,low", [(BF16, torch.finfo(BF16).min), (BF16, -math.inf), (FP16, -math.inf),
                                        (FP16, torch.finfo(FP16).min)], ids=str)
 def test_attention_masking_buckets(dtype, low):
@@ -424,6 +440,19 @@ def test_adamw_many_tensors_and_scaled_gradients():
         z = torch.zeros_like(w, dtype=torch.float64)
         want = ref.adamw(w.double(), gr.double() / 4, z, z, 1e-2, *HYPER["betas"], HYPER["eps"], 0.01, 7)[0]
         _close("param", t, want, 1e-6 * (want.abs() + 1e-2))
+
+
+def test_adamw_refuses_a_weight_twice():
+    p, g = _adamw_lists([100, 50], [BF16] * 2, [F32] * 2)
+    with pytest.raises(ValueError, match="twice"):
+        vswin.AdamW([p[0], p[1], p[0]])
+    opt = vswin.AdamW(p)
+    with pytest.raises(ValueError):
+        opt.step(g[:1])
+    with pytest.raises(ValueError, match=r"grads\[1\]"):
+        opt.step([g[0], g[1][:49]])
+    with pytest.raises(TypeError):
+        opt.step(g, step=torch.ones(1, device="cuda"))
 
 
 @pytest.mark.parametrize("bits", [32, 8])

@@ -63,7 +63,7 @@ def _rot(rows=8, dim=32, cos=11, sin=12, positions=None, inter=0):
     dict(rot=_rot(dim=33)), dict(rot=_rot(dim=66)), dict(rot=_rot(dim=-2)), dict(rot=_rot(cos=0)), dict(rot=_rot(sin=0)),
     dict(rot=_rot(rows=0)), dict(rot=_rot(rows=7)), dict(rot=_rot(positions=P(13, 2))),
     dict(back=dict(g=None)), dict(back=dict(g=P(10))), dict(back=dict(h=P(1, 64))), dict(back=dict(dq=_view(2, 8, 4, 64))),
-    dict(back=dict(dq=_view(7, 8, 4, 64, batch_stride=64))), dict(back=dict(dk=_view(7, 8, 2, 64))),
+    dict(hk=4, k=_view(1, 8, 4, 64), qo=_view(1, 8, 4, 64)), dict(back=dict(dq=_view(7, 8, 4, 64, batch_stride=64))), dict(back=dict(dk=_view(7, 8, 2, 64))),
 ], ids=str)
 def test_norm_refusals(L, kw):
     before = vswin.launch_count()
@@ -92,7 +92,7 @@ def _attn(L, dtype=0, B=2, Lq=8, Lk=8, hq=4, hk=2, d=64, q=None, k=None, v=None,
 
 @pytest.mark.parametrize("kw", [
     dict(dtype=5), dict(B=0), dict(Lq=0), dict(Lk=0), dict(hq=0), dict(hk=0), dict(d=0), dict(hq=3), dict(scale=math.nan),
-    dict(scale=math.inf), dict(table=0), dict(bmap=0), dict(buckets=0), dict(buckets=4097), dict(D=-1), dict(D=2**20 + 1),
+    dict(scale=math.inf), dict(scale=-2e30), dict(table=0), dict(bmap=0), dict(buckets=0), dict(buckets=513), dict(D=-1), dict(D=2**20 + 1),
     dict(lse=0), dict(q=_view(1, 8, 4, 64, off=8)), dict(k=_view(2, 8, 2, 64, token_stride=132)),
     dict(v=_view(0, 8, 2, 64)), dict(out=_view(1, 8, 4, 64)), dict(out=_view(2, 8, 4, 64, off=256)),
     dict(out=_view(6, 8, 4, 64, head_stride=0)), dict(lse=6), dict(lse=1),
