@@ -93,20 +93,20 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // heavy query tiles (causal: the last) first
-  const unsigned per_tile = (unsigned)a.B * a.hq * sp.n;
-  const unsigned id = gridDim.x - 1 - blockIdx.x;
-  const int qt = (int)(id / per_tile);
-  unsigned rest = id % per_tile;
-  const int split = (int)(rest % sp.n);
-  rest /= sp.n;
-  const int h = (int)(rest % a.hq), b = (int)(rest / a.hq), hk = h / (a.hq / a.hk);
+  // the tiles before sp.first whole, then those from there on in sp.n parts of the keys
+  const unsigned whole = sp.n > 1 ? (unsigned)sp.first : gridDim.x;
+  const unsigned extra = blockIdx.x < whole ? 0 : blockIdx.x - whole;
+  const bool is_split = blockIdx.x >= whole;
+  const int split = (int)(extra % sp.n), parts = is_split ? sp.n : 1;
+  const unsigned id = is_split ? whole + extra / sp.n : blockIdx.x;
+  const QueryTile q = query_tile(a, id);
+  const int h = q.h, b = q.b, hk = h / (a.hq / a.hk);
   const SeqLens sl = seq_lens(a, b);
-  const int i0 = qt * 128, pos0 = sl.start + i0;
+  const int i0 = q.qt * 128, pos0 = sl.start + i0;
   int nk = i0 < sl.nq ? sl.nk : 0;
   if (a.causal) nk = min(nk, max(0, sl.start + min(i0 + 128, sl.nq)));
   const int tiles = (nk + kBn - 1) / kBn;
-  const int per = (tiles + sp.n - 1) / sp.n;
+  const int per = (tiles + parts - 1) / parts;
   const int t0 = min(split * per, tiles), nt = min(t0 + per, tiles) - t0;
 
   if (tid == 0) {
@@ -326,14 +326,15 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       const bool some = i < sl.nq && (l > 0.f || l != l);
       const float inv = some ? 1.f / l : 0.f;
       const long long r = ((long long)b * a.hq + h) * a.Lq + i;
+      const long long pr = split * sp.rows + (is_split ? (long long)(id - sp.first) * 128 + row : 0);
       if (in && g == 0) {
-        if (sp.n == 1)
+        if (!is_split)
           a.lse[r] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
         else
-          sp.lse[(long long)split * a.B * a.hq * a.Lq + r] = some ? m + log2f(l) : -INFINITY;
+          sp.lse[pr] = some ? m + log2f(l) : -INFINITY;
       }
       T* out = static_cast<T*>(a.o.p) + (in ? a.o.at(b, i, h) : 0);
-      float* part = sp.o + ((long long)split * a.B * a.hq * a.Lq + (in ? r : 0)) * D;
+      float* part = sp.o + pr * D;
       // each group writes its part of the channels
 #pragma unroll
       for (int c0 = 0; c0 < D / G; c0 += 16) {
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
           for (int k = 0; k < 16; ++k)
             if (some && weight[e] != 0.f) f[k] = fmaf(__uint_as_float(u[k]), weight[e] * inv, f[k]);
         }
-        if (in && sp.n == 1) {
+        if (in && !is_split) {
 #pragma unroll
           for (int k = 0; k < 16; k += 8)
             *reinterpret_cast<uint4*>(out + ch + k) =
@@ -375,14 +376,17 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   }
 }
 
-// Parts of the keys when the query tiles alone leave SMs idle: as many as fill
-// two CTAs per SM, at least 512 keys in each.
-int forward_splits(const BiasAttnArgs& a) {
-  const long long ctas = (long long)a.B * a.hq * ((a.Lq + 127) / 128), slots = 2LL * sm_count();
-  const long long tiles = (a.Lk + 63) / 64;
-  if (2 * ctas > slots) return 1;
-  const long long parts = slots / ctas, most = tiles / 8;
-  return (int)(parts < most ? parts : (most < 1 ? 1 : most));
+// Tiles that are split over the keys: all of them when they fill at most half of
+// the resident CTAs (two per SM); else, when all tiles cost the same, those that
+// would run as a last wave of at most half of them. As many parts as fill one
+// wave, at least 512 keys in each.
+Split forward_split(const BiasAttnArgs& a) {
+  const long long tiles = (long long)a.B * a.hq * ((a.Lq + 127) / 128), wave = 2LL * sm_count();
+  long long last = 2 * tiles <= wave ? tiles : (a.causal ? 0 : tiles % wave);
+  if (2 * last > wave) last = 0;
+  const long long parts = last ? wave / last : 1, most = a.Lk / 512;
+  const int n = (int)(parts < most ? parts : (most < 1 ? 1 : most));
+  return n > 1 ? Split{n, last * 128, (int)(tiles - last), nullptr, nullptr} : Split{1, 0, 0, nullptr, nullptr};
 }
 
 template <class T, int D>
@@ -391,14 +395,16 @@ cudaError_t forward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
   static_assert(2 * (C::SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
   cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const Split sp = split_of(a, forward_splits(a), scratch);
+  Split sp = forward_split(a);
+  split_place(&sp, D, scratch);
   const int dtype = std::is_same<T, __half>::value ? kFP16 : kBF16;
   FwdParams params;
   params.a = a;
   make_head_map(&params.q, a.q, a.B, a.Lq, a.hq, D, dtype, 128);
   make_head_map(&params.k, a.k, a.B, a.Lk, a.hk, D, dtype, C::BN);
   make_head_map(&params.v, a.v, a.B, a.Lk, a.hk, D, dtype, C::BN);
-  const long long grid = (long long)a.B * a.hq * ((a.Lq + 127) / 128) * sp.n;
+  const long long tiles = (long long)a.B * a.hq * ((a.Lq + 127) / 128);
+  const long long grid = sp.n > 1 ? sp.first + (tiles - sp.first) * sp.n : tiles;
   prof_begin(kKindOther, st);
   attn_fwd_kernel<T, D><<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(params, sp);
   prof_end(kKindOther, st);
@@ -417,7 +423,7 @@ cudaError_t forward_d(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
 }  // namespace
 
 size_t bias_attention_scratch_bytes(const BiasAttnArgs& a) {
-  return split_bytes(a, token_form(a) ? token_splits(a) : forward_splits(a));
+  return split_bytes(token_form(a) ? token_split(a) : forward_split(a), a.d);
 }
 cudaError_t launch_bias_attention(const BiasAttnArgs& a, int dtype, void* scratch, cudaStream_t st) {
   if (token_form(a)) return launch_token_attention(a, dtype, scratch, st);

@@ -301,10 +301,29 @@ struct LineWriter {
     float value = base > a.D ? high : low;
     int which = base > a.D ? high_which : low_which;
     if (!flat) {
-      float v[(N + 31) / 32];
-      int k[(N + 31) / 32];
+      constexpr int kPer = (N + 31) / 32;
+      float v[kPer];
+      int k[kPer];
+      // the map's entries, then the table's: two rounds of loads in flight at once
 #pragma unroll
-      for (int t = 0; t < (N + 31) / 32; ++t) v[t] = entry(base + min(32 * t + lane, N - 1), &k[t]);
+      for (int t = 0; t < kPer; ++t) {
+        const int rel = base + min(32 * t + lane, N - 1);
+        k[t] = __ldg(a.map + min(max(rel, -a.D), a.D) + a.D);
+      }
+      bool bad = false;
+#pragma unroll
+      for (int t = 0; t < kPer; ++t) {
+        const bool in = (unsigned)k[t] < (unsigned)a.buckets;
+        bad = bad || !in;
+        k[t] = in ? k[t] : 0;
+        v[t] = in ? to_f(static_cast<const T*>(a.table)[(long long)k[t] * a.hq + h]) : 0.f;
+      }
+      if (bad) atomicCAS(a.ctx.err, 0, kErrBounds);
+#pragma unroll
+      for (int t = 0; t < kPer; ++t) {
+        const bool gone = v[t] <= kExclude || (a.causal && base + min(32 * t + lane, N - 1) > 0);
+        v[t] = gone ? -INFINITY : v[t] * kLog2E;
+      }
       value = __shfl_sync(0xffffffffu, v[0], 0);
       which = __shfl_sync(0xffffffffu, k[0], 0);
       flat = true;

@@ -7,17 +7,27 @@
 namespace vswin {
 
 struct Split {
-  int n;       // parts of the keys (1: results go out directly)
-  float* o;    // [n][B hq Lq][d]
-  float* lse;  // [n][B hq Lq], log2
+  int n;           // parts of the keys (1: results go out directly)
+  long long rows;  // rows that are split
+  int first;       // first split tile of 128 rows (rows by tile), or -1: rows are (b, h, i)
+  float* o;        // [n][rows][d]
+  float* lse;      // [n][rows], log2
 };
 
-inline size_t split_bytes(const BiasAttnArgs& a, int n) {
-  return n > 1 ? (size_t)n * a.B * a.hq * a.Lq * (a.d + 1) * 4 : 0;
+inline size_t split_bytes(const Split& s, int d) { return s.n > 1 ? (size_t)s.n * s.rows * (d + 1) * 4 : 0; }
+inline void split_place(Split* s, int d, void* scratch) {
+  s->o = static_cast<float*>(scratch);
+  s->lse = s->n > 1 ? s->o + (size_t)s->n * s->rows * d : nullptr;
 }
-inline Split split_of(const BiasAttnArgs& a, int n, void* scratch) {
-  float* o = static_cast<float*>(scratch);
-  return Split{n, o, n > 1 ? o + (size_t)n * a.B * a.hq * a.Lq * a.d : nullptr};
+
+// Query tile `tile` of a launch: head and batch fastest, the last rows first.
+struct QueryTile {
+  int b, h, qt;
+};
+__host__ __device__ inline QueryTile query_tile(const BiasAttnArgs& a, unsigned tile) {
+  const unsigned heads = (unsigned)a.B * a.hq, tiles = (unsigned)(a.Lq + 127) / 128;
+  const unsigned rest = tile % heads;
+  return {(int)(rest / a.hq), (int)(rest % a.hq), (int)(tiles - 1 - tile / heads)};
 }
 
 template <class T, int D>
@@ -25,7 +35,7 @@ cudaError_t launch_attention_join(const BiasAttnArgs& a, const Split& sp, cudaSt
 
 // The form for few rows (bias_attention_token.cu).
 bool token_form(const BiasAttnArgs& a);
-int token_splits(const BiasAttnArgs& a);
+Split token_split(const BiasAttnArgs& a);
 cudaError_t launch_token_attention(const BiasAttnArgs& a, int dtype, void* scratch, cudaStream_t st);
 
 }  // namespace vswin

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
   const bool some = i < sl.nq && top > -INFINITY;
   const float inv = some ? 1.f / total : 0.f;
   const long long at = ((long long)b * a.hq + h) * a.Lq + i;
-  const long long out_rows = (long long)a.B * a.hq * a.Lq;
+  const long long out_rows = sp.rows;
   if (part == 0) {
     if (sp.n == 1)
       a.lse[at] = some ? (top + log2f(total)) * kLn2 : -INFINITY;
@@ -265,10 +265,18 @@ __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
 // The parts of the keys joined: a row per warp.
 template <class T, int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ BiasAttnArgs a, Split sp) {
-  const long long rows = (long long)a.B * a.hq * a.Lq;
+  const long long rows = sp.rows;
   const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
+  int i, h, b;
+  if (sp.first < 0) {
+    i = (int)(r % a.Lq), h = (int)(r / a.Lq % a.hq), b = (int)(r / a.Lq / a.hq);
+  } else {
+    const QueryTile q = query_tile(a, (unsigned)(sp.first + r / 128));
+    i = q.qt * 128 + (int)(r % 128), h = q.h, b = q.b;
+    if (i >= a.Lq) return;
+  }
   float top = -INFINITY;
   bool nan = false;
   for (int s = lane; s < sp.n; s += 32) {
@@ -291,13 +299,12 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
       for (int k = 0; k < D / 32; ++k) v[k] = fmaf(w, sp.o[(s * rows + r) * D + lane + 32 * k], v[k]);
     }
   }
-  const int i = (int)(r % a.Lq), h = (int)(r / a.Lq % a.hq), b = (int)(r / a.Lq / a.hq);
   if (nan) total = top = __int_as_float(0x7fffffff);
   const float inv = total > 0.f || nan ? 1.f / total : 0.f;
   T* out = static_cast<T*>(a.o.p) + a.o.at(b, i, h);
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) out[lane + 32 * k] = from_f<T>(v[k] * inv);
-  if (lane == 0) a.lse[r] = top > -INFINITY || nan ? (top + log2f(total)) * kLn2 : -INFINITY;
+  if (lane == 0) a.lse[((long long)b * a.hq + h) * a.Lq + i] = top > -INFINITY || nan ? (top + log2f(total)) * kLn2 : -INFINITY;
 }
 
 // Parts of the keys: enough CTAs for two waves of what is resident (sequences
@@ -317,7 +324,8 @@ cudaError_t token(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
   token_plan(a, &blocks, &n);
   cudaError_t e = cudaFuncSetAttribute(attn_token_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const Split sp = split_of(a, n, scratch);
+  Split sp = token_split(a);
+  split_place(&sp, D, scratch);
   prof_begin(kKindOther, st);
   attn_token_kernel<T, D><<<(unsigned)((long long)a.B * a.hk * blocks * n), 32 * kWarps, C::SMEM, st>>>(a, sp, blocks);
   prof_end(kKindOther, st);
@@ -337,9 +345,8 @@ cudaError_t token_d(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
 
 template <class T, int D>
 cudaError_t launch_attention_join(const BiasAttnArgs& a, const Split& sp, cudaStream_t st) {
-  const long long rows = (long long)a.B * a.hq * a.Lq;
   prof_begin(kKindOther, st);
-  attn_join_kernel<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, sp);
+  attn_join_kernel<T, D><<<(unsigned)((sp.rows + 3) / 4), 128, 0, st>>>(a, sp);
   prof_end(kKindOther, st);
   count_launch();
   return cudaGetLastError();
@@ -354,10 +361,10 @@ template cudaError_t launch_attention_join<__half, 128>(const BiasAttnArgs&, con
 // Up to 64 rows per key head (four blocks of 16, which share the keys in L2).
 bool token_form(const BiasAttnArgs& a) { return (long long)a.Lq * (a.hq / a.hk) <= 64; }
 
-int token_splits(const BiasAttnArgs& a) {
+Split token_split(const BiasAttnArgs& a) {
   int blocks, n;
   token_plan(a, &blocks, &n);
-  return n;
+  return Split{n, (long long)a.B * a.hq * a.Lq, -1, nullptr, nullptr};
 }
 
 cudaError_t launch_token_attention(const BiasAttnArgs& a, int dtype, void* scratch, cudaStream_t st) {

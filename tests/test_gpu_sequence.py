@@ -311,6 +311,13 @@ def test_attention_new_tokens(case, causal):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("d", [32, 128])
+def test_attention_last_wave_in_parts(d):
+    # 300 query tiles: the four behind the first wave of 296 run as parts of the keys
+    ins, _ = _attn_inputs(BF16, 2, 70, 1100, 150, 50, d)
+    _attn_check(ins, _map(), None, backward=False, kv_lens=_i32(1100, 530), q_start=_i32(500, 0), q_lens=_i32(70, 66))
+
+
 def test_attention_offsets_past_32_bits():
     # the second sequence's cache starts 2^31 elements in, the query's rows lie 2^31 elements apart
     d, Lk = 64, 300
