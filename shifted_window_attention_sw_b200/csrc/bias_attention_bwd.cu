@@ -21,9 +21,10 @@
 //
 // The table's gradient sums dS along diagonals (the bias is one line per tile,
 // see BiasLine). A tile of one bucket adds its rows' sums. In the others a
-// warp passes partial sums from lane to lane: after column c, lane 31 holds the
-// finished sum of diagonal c - 31; the 63 diagonals of its 32 x 32 part then go to
-// the warp's bins, equal buckets combined in lane order.
+// warp passes partial sums from lane to lane, in four runs of eight columns: after
+// column c of a run, lane 31 holds the run's sum of diagonal c - 31. The 63
+// diagonals of the warp's 32 x 32 part, the runs added, then go to its bins, equal
+// buckets combined in lane order.
 #include "bias_attention.cuh"
 
 namespace vswin {
@@ -46,7 +47,7 @@ struct BwdCfg {
   static constexpr int OFF_LINE = OFF_M + ST * 2 * kMoving;
   static constexpr int OFF_COL = OFF_LINE + (ST * (int)sizeof(Line) + 15) / 16 * 16;  // per stage and column (-lse, -D)
   static constexpr int OFF_DIAG = OFF_COL + (kKeys ? ST * kBn * 8 : 0);
-  static constexpr int OFF_BAR = OFF_DIAG + (kKeys ? 0 : kWarps * 64 * 4);
+  static constexpr int OFF_BAR = OFF_DIAG + (kKeys ? 0 : kWarps * 160 * 4);
   static constexpr int OFF_BINS = OFF_BAR + 192;                    // [kWarps][buckets], queries fixed
   static constexpr uint32_t kTmem = D == 128 ? 512 : 256;
   static constexpr int kColAcc = 128 * G;  // sums behind the score buffers
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     const float c = a.scale * kLog2E;
     const float2 c2 = make_float2(c, c);
     float* bins = reinterpret_cast<float*>(smem + C::OFF_BINS) + warp * a.buckets;
-    float* diag = reinterpret_cast<float*>(smem + C::OFF_DIAG) + warp * 64;
+    float* diag = reinterpret_cast<float*>(smem + C::OFF_DIAG) + warp * 160;  // [4][40]
     float nl = -INFINITY, nd = 0.f;  // queries fixed: -lse (log2) and -D of the row
     float flat_sum = 0.f;            // dS of tiles of one bucket, until the bucket changes
     int flat_bucket = 0;
@@ -285,7 +286,6 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
       const float2* col = cols + s * kBn;
       const int live = kKeys ? kBn : m_hi - t * kBn;  // queries fixed: columns of the tile that are keys
       float2 sum = make_float2(0.f, 0.f);
-      float acc = 0.f;
       if (!kKeys && flat && bl.which != flat_bucket) {
         flush_flat();
         flat_bucket = bl.which;
@@ -333,12 +333,20 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
           // over scores of this half that have been read
           if (kKeys) tmem_st8(buf + c_first + e / 2, wp);
           tmem_st8(buf + 64 + c_first + e / 2, w);
-          if (!kKeys && !kFlat) {
+          if (!kKeys && !kFlat) {  // two runs of eight columns side by side
+            float acc[2] = {0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float up = __shfl_up_sync(0xffffffffu, acc, 1);
-              acc = (lane == 0 ? 0.f : up) + ds[k];
-              if (lane == 31) diag[e + k] = acc;
+            for (int k = 0; k < 8; ++k) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float up = __shfl_up_sync(0xffffffffu, acc[x], 1);
+                acc[x] = (lane == 0 ? 0.f : up) + ds[8 * x + k];
+                if (lane == 31) diag[(e / 8 + x) * 40 + k] = acc[x];
+              }
+            }
+            if (lane < 31) {
+              diag[e / 8 * 40 + 38 - lane] = acc[0];
+              diag[(e / 8 + 1) * 40 + 38 - lane] = acc[1];
             }
           }
         }
@@ -364,36 +372,44 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
         if (flat) {
           flat_sum += sum.x + sum.y;
         } else {
-          if (lane < 31) diag[62 - lane] = acc;
           __syncwarp();
+          float v[2] = {0.f, 0.f};
+          int bucket[2], start[2];
+          uint32_t heads[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int at = lane + 32 * k;  // diagonal at - 31 of the warp's 32 x 32
-            const bool have = at < 63;
-            float v = have ? diag[at] : 0.f;
-            const int bucket = have ? bl.bucket[at + 96 + c_first - 32 * (warp & 3)] : -1;
-            // a run of one bucket adds up into its last lane
-            const int before = __shfl_up_sync(0xffffffffu, bucket, 1);
-            const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 || before != bucket);
-            const int start = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));
 #pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-              const float x = __shfl_up_sync(0xffffffffu, v, o);
-              if (lane - o >= start) v += x;
-            }
-            const bool tail = lane == 31 || ((heads >> (lane + 1)) & 1);
+            for (int x = 0; x < 4; ++x)
+              if (at >= 8 * x && at - 8 * x < 39) v[k] += diag[x * 40 + at - 8 * x];
+            bucket[k] = at < 63 ? bl.bucket[at + 96 + c_first - 32 * (warp & 3)] : -1;
+            const int before = __shfl_up_sync(0xffffffffu, bucket[k], 1);
+            heads[k] = __ballot_sync(0xffffffffu, lane == 0 || before != bucket[k]);
+            start[k] = 31 - __clz(heads[k] & (0xffffffffu >> (31 - lane)));
+          }
+          // a run of one bucket adds up into its last lane
+#pragma unroll
+          for (int o = 1; o < 32; o *= 2) {
+            const float x[2] = {__shfl_up_sync(0xffffffffu, v[0], o), __shfl_up_sync(0xffffffffu, v[1], o)};
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (lane - o >= start[k]) v[k] += x[k];
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool tail = bucket[k] >= 0 && (lane == 31 || ((heads[k] >> (lane + 1)) & 1));
             // runs that share a bucket (no map of vswin_bucket_map has them) add up into the first
-            const uint32_t equal = __match_any_sync(0xffffffffu, tail && have ? bucket : -2 - lane);
+            const uint32_t equal = __match_any_sync(0xffffffffu, tail ? bucket[k] : -2 - lane);
             const bool first = (equal & ((1u << lane) - 1)) == 0;
             uint32_t others = first ? equal & ~(1u << lane) : 0;
             while (__any_sync(0xffffffffu, others != 0)) {
-              const float x = __shfl_sync(0xffffffffu, v, others ? __ffs(others) - 1 : lane);
+              const float x = __shfl_sync(0xffffffffu, v[k], others ? __ffs(others) - 1 : lane);
               if (others) {
-                v += x;
+                v[k] += x;
                 others &= others - 1;
               }
             }
-            if (tail && have && first) bins[bucket] += v;
+            if (tail && first) bins[bucket[k]] += v[k];
             __syncwarp();
           }
         }
