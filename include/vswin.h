@@ -381,7 +381,11 @@ typedef struct {
  * q_start (0) the position of its query 0; query i stands at q_start + i, key j
  * at j. causal: key j is seen up to j <= q_start + i. What lies behind the
  * lengths is never used, whatever it holds. Lengths outside [0, Lq] or [0, Lk]
- * are clamped and reported by vswin_poll_error (VSWIN_ERR_BOUNDS). */
+ * are clamped and reported by vswin_poll_error (VSWIN_ERR_BOUNDS). A key below
+ * kv_lens that a query does not see (causal, or a bias that takes it out) has
+ * probability 0 for it whatever k holds, but its v has to be finite: 0 times it
+ * is part of the sum. The backward entry wants q, k, v and dout finite below
+ * the lengths. */
 typedef struct {
   const int* q_lens;
   const int* kv_lens;
@@ -413,7 +417,8 @@ int vswin_bias_attention_forward(int dtype, int B, int Lq, int Lk, int hq, int h
  * and dtable [buckets][hq], all of the tensors' type, summed in fp32 and rounded
  * once, overwritten. Zero for rows and keys that take no part. The gradients
  * overlap no input; dq, dk and dv may be slices of one buffer. Scratch: from the
- * library's pool, 4 bytes per query row and head plus the table's sums.
+ * library's pool, 4 bytes per query row and head and 4 bytes per bucket, head
+ * and 128 query rows of a sequence.
  */
 int vswin_bias_attention_backward(int dtype, int B, int Lq, int Lk, int hq, int hk, int d, const vswin_heads* q,
                                   const vswin_heads* k, const vswin_heads* v, float scale,

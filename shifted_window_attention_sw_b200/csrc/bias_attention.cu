@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   uint64_t* o_done = p_full + kRing;  // [kRing] P V accumulated (V has been read)
   uint64_t* q_full = o_done + kRing;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_full + 1);
+  uint32_t* gave_up = s_tmem + 1;  // a wait ran out
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       mbar_init(&o_done[k], 1);
     }
     mbar_init(q_full, 1);
+    *gave_up = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       if (nt > 0) bring_tile<T, D, 128>(sq, params.q, a.q, b, h, i0, sl.nq, a.Lq, q_full);
       // K runs a tile ahead of V: its stage is free a tile earlier
       auto wait_tile = [&](uint64_t* done, int t) {
-        return t < 0 || warp_wait(&done[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnLoad);
+        return t < 0 || warp_wait(&done[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnLoad, gave_up);
       };
       for (int t = 0; t <= nt; ++t) {
         if (t < nt) {
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     } else if (nt > 0) {
       const LineWriter<T, C::kLineN, false> writer(a, h);
       for (int t = 0; t < nt; ++t) {
-        if (t >= kRing && !warp_wait(&p_full[t % kRing], (t / kRing - 1) & 1, a.ctx, kErrAttnLoad)) break;
+        if (t >= kRing && !warp_wait(&p_full[t % kRing], (t / kRing - 1) & 1, a.ctx, kErrAttnLoad, gave_up)) break;
         writer.write(&lines[t % kRing], (t0 + t) * kBn - pos0 - 127);
         if (lane == 0) mbar_arrive(&s_full[t % kRing]);
       }
@@ -165,8 +167,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       mma_rows<D, kBn>(tmem + kBn * (t % NBUF), sq, sk + t % ST * C::kTile, id_s);
       umma_commit(&s_full[t % kRing]);
     };
-    auto wait_k = [&](int t) { return warp_wait(&k_full[t % ST], (t / ST) & 1, a.ctx, kErrAttnMma); };
-    bool ok = nt > 0 && warp_wait(q_full, 0, a.ctx, kErrAttnMma);
+    auto wait_k = [&](int t) { return warp_wait(&k_full[t % ST], (t / ST) & 1, a.ctx, kErrAttnMma, gave_up); };
+    bool ok = nt > 0 && warp_wait(q_full, 0, a.ctx, kErrAttnMma, gave_up);
     for (int t = 0; t < NBUF && t < nt && ok; ++t) {
       ok = wait_k(t);
       if (!ok) break;
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     }
     for (int t = 0; t < nt && ok; ++t) {
       const int u = t + NBUF;  // the tile whose scores take this one's buffer
-      ok = warp_wait(&p_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnMma);
+      ok = warp_wait(&p_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnMma, gave_up);
       if (!ok) break;
       // the scores that follow go out at once when their keys are there
       const bool now = u < nt && __all_sync(0xffffffffu, mbar_test(&k_full[u % ST], (u / ST) & 1));
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     constexpr int kPart = kBn / 2;  // columns in registers at a time (80 or 128 registers)
     bool ok = true;
     for (int t = g; t < nt; t += G) {
-      ok = warp_wait(&s_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnSoftmax);
+      ok = warp_wait(&s_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up);
       if (!ok) break;
       tc_fence_after();
       const uint32_t buf = tw + kBn * (t % NBUF);
@@ -217,10 +219,12 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       const float value = bl.value;
       const float* line = bl.line + 127 - row;
       const int live = nk - (t0 + t) * kBn;  // columns of the tile that are keys
-      // one part of the tile: of one bucket or not, with keys missing or not
-      auto part = [&](auto second_, auto flat_, auto cut_) {
+      // one part of the tile: of one bucket or not, with keys missing or not; kRedo when a score is NaN, then again
+      // with `careful`, where NaN or infinity in a key that the bias or the causal rule takes out does not count
+      enum { kFailed, kDone, kRedo };
+      auto part = [&](auto second_, auto flat_, auto cut_, auto careful_) -> int {
         constexpr int c0 = decltype(second_)::value ? kPart : 0;
-        constexpr bool kFlat = decltype(flat_)::value, kCut = decltype(cut_)::value;
+        constexpr bool kFlat = decltype(flat_)::value, kCut = decltype(cut_)::value, kCareful = decltype(careful_)::value;
         uint32_t u[kPart];
 #pragma unroll
         for (int e = 0; e < kPart; e += 32) tmem_ld32(buf + c0 + e, u + e);
@@ -230,17 +234,28 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
 #pragma unroll
         for (int k = 0; k < kPart; k += 2) {
           float2 y = make_float2(off, off);
-          if (!kFlat) y = __fadd2_rn(make_float2(line[c0 + k], line[c0 + k + 1]), y);
+          float2 bias;
+          if (!kFlat) {
+            bias = kCareful && flat ? make_float2(value, value) : make_float2(line[c0 + k], line[c0 + k + 1]);
+            y = __fadd2_rn(bias, y);
+          }
           y = __ffma2_rn(make_float2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), c2, y);
           x[k] = !kCut || c0 + k < live ? y.x : -INFINITY;
           x[k + 1] = !kCut || c0 + k + 1 < live ? y.y : -INFINITY;
+          if (kCareful && bias.x == -INFINITY) x[k] = -INFINITY;
+          if (kCareful && bias.y == -INFINITY) x[k + 1] = -INFINITY;
         }
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto largest = [&](auto max_of) {
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < kPart; k += 2) tops[k / 2 % 4] = max3(tops[k / 2 % 4], x[k], x[k + 1]);
-        const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
-        const bool move = l == 0.f ? top > -INFINITY : top > kSlack;
-        if (__any_sync(0xffffffffu, move)) {
+          for (int k = 0; k < kPart; k += 2) tops[k / 2 % 4] = max_of(tops[k / 2 % 4], x[k], x[k + 1]);
+          return max_of(max_of(tops[0], tops[1], tops[2]), tops[3], tops[3]);
+        };
+        const float top = kCareful ? largest(max3) : largest(max3_nan);
+        // (unordered comparisons: a NaN enters, too)
+        if (__any_sync(0xffffffffu, l == 0.f ? top != -INFINITY : !(top <= kSlack))) {
+          if (!kCareful && __any_sync(0xffffffffu, top != top)) return kRedo;
+          const bool move = l == 0.f ? top > -INFINITY : top > kSlack;
           // by whole powers of two, so that what is there already is rescaled without rounding
           const float step = move ? ceilf(top) : 0.f;
           const float alpha = step < 127.f ? __int_as_float((127 - max((int)step, 0)) << 23) : 0.f;
@@ -262,7 +277,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
             }
           }
           if (t >= G) {  // (the group's sums so far: complete before these scores were, or waited for)
-            if (G == 1 && !warp_wait(&o_done[(t - 1) % kRing], ((t - 1) / kRing) & 1, a.ctx, kErrAttnSoftmax)) return false;
+            if (G == 1 && !warp_wait(&o_done[(t - 1) % kRing], ((t - 1) / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up)) return kFailed;
             tc_fence_after();
 #pragma unroll
             for (int e = 0; e < D; e += 8) {
@@ -288,13 +303,18 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
           tmem_st8(buf + (c0 + e) / 2, v);  // over scores that have been read
         }
         l += acc.x + acc.y;
-        return true;
-      };
-      auto tile = [&](auto flat_, auto cut_) {
-        return part(std::false_type{}, flat_, cut_) && (kPart == kBn || part(std::true_type{}, flat_, cut_));
+        return kDone;
       };
       using Yes = std::true_type;
       using No = std::false_type;
+      auto tile = [&](auto flat_, auto cut_) {
+        int r = part(No{}, flat_, cut_, No{});
+        if (r == kRedo) r = part(No{}, No{}, Yes{}, Yes{});
+        if (r == kFailed) return false;
+        r = part(Yes{}, flat_, cut_, No{});
+        if (r == kRedo) r = part(Yes{}, No{}, Yes{}, Yes{});
+        return r != kFailed;
+      };
       if (live >= kBn)
         ok = flat ? tile(Yes{}, No{}) : tile(No{}, No{});
       else
@@ -306,7 +326,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       if (lane == 0) mbar_arrive(&p_full[t % kRing]);
     }
     const int last = nt - 1 - (G == 2 ? (nt - 1 - g) & 1 : 0);  // the group's last tile
-    if (ok && last >= 0) ok = warp_wait(&o_done[last % kRing], (last / kRing) & 1, a.ctx, kErrAttnSoftmax);
+    if (ok && last >= 0) ok = warp_wait(&o_done[last % kRing], (last / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up);
     tc_fence_after();
     // the groups' sums over their tiles of the row, weighed against the larger reference; a group without any has weight 0
     float weight[2] = {1.f, 0.f};
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     }
     tc_fence_before();
   }
-  __syncthreads();
+  join_roles(gave_up);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);

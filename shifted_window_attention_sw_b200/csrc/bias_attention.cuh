@@ -70,9 +70,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Largest of three, NaN set aside.
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+// The same, NaN when one of them is.
+__device__ __forceinline__ float max3_nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
 
@@ -219,10 +227,11 @@ __device__ __forceinline__ void bring_tile(uint32_t dst, const HeadMap& m, const
   }
 }
 
-// A whole warp waits; false in every lane when the wait gave up (as mbar_wait
-// does). The hardware suspends the warp for up to the hint (ns) per try: waiting
+// A whole warp waits; false in every lane, and *gave_up set, when the wait gave
+// up (as mbar_wait does). The hardware suspends the warp for up to the hint (ns) per try: waiting
 // warps that poll more often take issue slots from the working ones.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtx& ctx, int code) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtx& ctx, int code,
+                                          uint32_t* gave_up) {
   auto once = [&]() {
     uint32_t ok;
     asm volatile(
@@ -239,10 +248,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   while (!once()) {
     if (__any_sync(0xffffffffu, global_timer_ns() - t0 > ctx.wait_limit)) {
       if ((threadIdx.x & 31) == 0) atomicCAS(ctx.err, 0, code);
+      *gave_up = 1;
       return false;
     }
   }
   return true;
+}
+
+// Where a kernel's roles meet at its end. When a wait gave up (`gave_up`, in
+// shared memory), copies and MMAs may still be under way: they get a millisecond
+// to land before shared memory and TMEM are given back.
+__device__ __forceinline__ void join_roles(const volatile uint32_t* gave_up) {
+  __syncthreads();
+  if (*gave_up) {
+    const uint64_t t0 = global_timer_ns();
+    for (int k = 0; k < 100000 && global_timer_ns() - t0 < 1000000; ++k) __nanosleep(1000);
+  }
 }
 
 // One lane of a converged warp, which the compiler knows to be one: MMAs issued
@@ -261,8 +282,8 @@ __device__ __forceinline__ bool elect_one() {
 // it is one line of N = 127 + BN values, entry t at offset base + t: row i and
 // column j read entry j - i + 127 (rows are queries) or i - j + BN - 1 (rows are
 // keys). A line whose entries are all the same (`flat`; far tiles have one
-// bucket) is only `value` and its bucket `which`. With kBuckets the buckets are
-// kept too, and entries are the same only if their buckets are.
+// bucket) is only `value` and its bucket `which`. With kBuckets the
+// buckets are kept too, and entries are the same only if their buckets are.
 template <int N, bool kBuckets>
 struct BiasLine {
   float line[N + 1];

@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
   uint64_t* f_full = ds_full + G;         // fixed tiles
   uint64_t* done = f_full + 1;            // every sum accumulated
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* gave_up = s_tmem + 1;         // a wait ran out
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ft = (int)((gridDim.x - 1 - blockIdx.x) / (a.B * (kKeys ? a.hk : a.hq)));
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     }
     mbar_init(f_full, 2);
     mbar_init(done, 1);
+    *gave_up = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
         bring_tile<T, D, 128>(sf + C::kFixed, args.f2, F2, b, hf, f0, fn, fL, f_full);
       }
       for (int t = 0; t < nt; ++t) {
-        if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad)) break;
+        if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad, gave_up)) break;
         const int hm = kKeys ? h : hk;
         const uint32_t dst = sm + s * 2 * C::kMoving;
         bring_tile<T, D, kBn>(dst, args.m1, M1, b, hm, r0, mn, mL, &full[s]);
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     } else if (nt > 0) {
       LineWriter<T, kLineN, !kKeys> writer(a, h);
       for (int t = 0; t < nt; ++t) {
-        if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad)) break;
+        if (t >= ST && !warp_wait(&free_[s], parity, a.ctx, kErrAttnLoad, gave_up)) break;
         if constexpr (kKeys) {
 #pragma unroll
           for (int e = 0; e < kBn; e += 32) {
@@ -192,8 +194,8 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
       mma_rows<D, kBn>(buf + 64, sf + C::kFixed, m1 + C::kMoving, id_s);
       umma_commit(&s_full[t % G]);
     };
-    auto wait_tile = [&](int t) { return warp_wait(&full[t % ST], (t / ST) & 1, a.ctx, kErrAttnMma); };
-    bool ok = nt > 0 && warp_wait(f_full, 0, a.ctx, kErrAttnMma);
+    auto wait_tile = [&](int t) { return warp_wait(&full[t % ST], (t / ST) & 1, a.ctx, kErrAttnMma, gave_up); };
+    bool ok = nt > 0 && warp_wait(f_full, 0, a.ctx, kErrAttnMma, gave_up);
     for (int t = 0; t < G && t < nt && ok; ++t) {
       ok = wait_tile(t);
       if (!ok) break;
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     }
     for (int t = 0; t < nt && ok; ++t) {
       const int u = t + G;  // the tile whose scores take this one's buffer
-      ok = warp_wait(&ds_full[t % G], (t / G) & 1, a.ctx, kErrAttnMma);
+      ok = warp_wait(&ds_full[t % G], (t / G) & 1, a.ctx, kErrAttnMma, gave_up);
       if (!ok) break;
       // the scores that follow go out at once when their tiles are there
       const bool now = u < nt && __all_sync(0xffffffffu, mbar_test(&full[u % ST], (u / ST) & 1));
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     uint32_t sp = 0;
     bool ok = true;
     for (int t = g; t < nt; t += G) {
-      ok = warp_wait(&full[s], sp, a.ctx, kErrAttnSoftmax) && warp_wait(&s_full[g], (t / G) & 1, a.ctx, kErrAttnSoftmax);
+      ok = warp_wait(&full[s], sp, a.ctx, kErrAttnSoftmax, gave_up) && warp_wait(&s_full[g], (t / G) & 1, a.ctx, kErrAttnSoftmax, gave_up);
       if (!ok) break;
       tc_fence_after();
       const Line& bl = lines[s];
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
       if (s >= ST) s -= ST, sp ^= 1;
     }
     if (!kKeys) flush_flat();
-    if (ok && nt > 0) ok = warp_wait(done, 0, a.ctx, kErrAttnSoftmax);
+    if (ok && nt > 0) ok = warp_wait(done, 0, a.ctx, kErrAttnSoftmax, gave_up);
     tc_fence_after();
     if (ok) {
       // every quad writes its part of the sums' columns: dq, or dk and then dv
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
     }
     tc_fence_before();
   }
-  __syncthreads();
+  join_roles(gave_up);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);

@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
         const int e = k >> 1, j = j0 + 8 * t + 2 * qc + (k & 1);
         const float bias = far_piece ? far[e] : bias_of<T>(a, j - pos[e], head[e]) * kLog2E;
         float x = fmaf(s[t][k], c, bias);
-        if (!whole && (j >= j_hi || (a.causal && j > pos[e]))) x = -INFINITY;
+        // (a score of NaN or infinity plus a bias of -inf would be NaN)
+        if (bias == -INFINITY || (!whole && (j >= j_hi || (a.causal && j > pos[e])))) x = -INFINITY;
         s[t][k] = x;
         top[e] = fmaxf(top[e], x);
       }

@@ -72,6 +72,7 @@ _LL = ctypes.c_longlong
 
 # vswin_dtype
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+DTYPE_OF = {number: dtype for dtype, number in DTYPES.items()}
 ADAMW_BLOCK = 256  # elements that share one scale of the 8-bit moments
 
 
@@ -473,6 +474,14 @@ def _run(fn, dev, stream, *args):
         raise VswinError(status, last_error())
 
 
+def _new(stream, shape, dtype, device):
+    """Memory for a result, from the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(q.shape)} and {tuple(k.shape)}")
@@ -505,8 +514,8 @@ def qk_norm_forward(q, k, gamma_q, gamma_k, eps=1e-6, cos=None, sin=None, positi
     them) of the float32 tables cos and sin, in one pass; bf16, fp16 or fp32. Views with contiguous channels
     are taken as they are. ``q_out`` may be ``q`` and ``k_out`` ``k``. Returns (q_out, k_out)."""
     (B, L, hq, hk, d, dt, dev), args = _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
-    q_out = q.new_empty((B, L, hq, d)) if q_out is None else q_out
-    k_out = q.new_empty((B, L, hk, d)) if k_out is None else k_out
+    q_out = _new(stream, (B, L, hq, d), dt, dev) if q_out is None else q_out
+    k_out = _new(stream, (B, L, hk, d), dt, dev) if k_out is None else k_out
     _run(lib().vswin_qk_norm_forward, dev, stream, *args, _heads("q_out", q_out, (B, L, hq, d), dt, dev),
          _heads("k_out", k_out, (B, L, hk, d), dt, dev))
     return q_out, k_out
@@ -517,9 +526,9 @@ def qk_norm_backward(q, k, gamma_q, gamma_k, dq_out, dk_out, eps=1e-6, cos=None,
     """Gradients (dq, dk in the type of q; dgamma_q, dgamma_k float32) of qk_norm_forward for the output
     gradients ``dq_out`` and ``dk_out``. ``dq`` and ``dk`` may be given, e.g. as slices of one buffer."""
     (B, L, hq, hk, d, dt, dev), args = _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
-    dq = q.new_empty((B, L, hq, d)) if dq is None else dq
-    dk = q.new_empty((B, L, hk, d)) if dk is None else dk
-    dgamma = torch.empty((2, d), dtype=torch.float32, device=dev)
+    dq = _new(stream, (B, L, hq, d), dt, dev) if dq is None else dq
+    dk = _new(stream, (B, L, hk, d), dt, dev) if dk is None else dk
+    dgamma = _new(stream, (2, d), torch.float32, dev)
     at = dgamma.data_ptr()
     _run(lib().vswin_qk_norm_backward, dev, stream, *args, _heads("dq_out", dq_out, (B, L, hq, d), dt, dev),
          _heads("dk_out", dk_out, (B, L, hk, d), dt, dev), _heads("dq", dq, (B, L, hq, d), dt, dev),
@@ -569,8 +578,8 @@ def bias_attention_forward(q, k, v, table, bucket_map, scale=None, causal=False,
     cache: Lq = 1, q_start = kv_lens - 1. Returns (out, lse), lse float32 (B, hq, Lq)."""
     (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
                                                                  kv_lens, q_start)
-    out = q.new_empty((B, Lq, hq, d)) if out is None else out
-    lse = torch.empty((B, hq, Lq), dtype=torch.float32, device=dev) if lse is None else lse
+    out = _new(stream, (B, Lq, hq, d), dt, dev) if out is None else out
+    lse = _new(stream, (B, hq, Lq), torch.float32, dev) if lse is None else lse
     _run(lib().vswin_bias_attention_forward, dev, stream, *args, _heads("out", out, (B, Lq, hq, d), dt, dev),
          _flat("lse", lse, (B, hq, Lq), torch.float32, dev))
     return out, lse
@@ -583,8 +592,8 @@ def bias_attention_backward(q, k, v, table, bucket_map, out, lse, dout, scale=No
     (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
                                                                  kv_lens, q_start)
     qs, ks = (B, Lq, hq, d), (B, Lk, hk, d)
-    dq, dk, dv = (q.new_empty(s) if t is None else t for t, s in ((dq, qs), (dk, ks), (dv, ks)))
-    dtable = torch.empty_like(table)
+    dq, dk, dv = (_new(stream, s, dt, dev) if t is None else t for t, s in ((dq, qs), (dk, ks), (dv, ks)))
+    dtable = _new(stream, table.shape, dt, dev)
     _run(lib().vswin_bias_attention_backward, dev, stream, *args, _heads("out", out, qs, dt, dev),
          _flat("lse", lse, (B, hq, Lq), torch.float32, dev), _heads("dout", dout, qs, dt, dev),
          _heads("dq", dq, qs, dt, dev), _heads("dk", dk, ks, dt, dev), _heads("dv", dv, ks, dt, dev), dtable.data_ptr())
@@ -594,7 +603,8 @@ def bias_attention_backward(q, k, v, table, bucket_map, out, lse, dout, scale=No
 # ------------------------------------------------------------------ optimizer
 class AdamW:
     """AdamW over a list of contiguous weights on one CUDA device (see vswin_adamw_step): every step is one
-    launch per 192 tensors. The object owns the moments (zeros, or the ones given) and keeps the weights' list.
+    launch per 192 tensors. The object owns the moments (zeros, or the ones given) and keeps the weights' list;
+    a weight may get another storage (``p.data = ...``), a moment or master is loaded by copying into it.
 
     weight_decay: one value or one per weight. bits: 32 (float32 moments) or 8 (codes with a scale per 256
     elements). master: float32 copies that are stepped and rounded into the weights: True makes them, or a list.
@@ -674,6 +684,9 @@ class AdamW:
                                  f"got {g.dtype} {tuple(g.shape)} on {g.device}")
             r.grad = g.data_ptr()
             r.grad_dtype = dt
+            p = self.params[i]
+            if p.data_ptr() != r.param:  # its storage was exchanged
+                r.param = _flat(("params", i), p, shape, DTYPE_OF[r.param_dtype], dev)
         count, count_dev = self.steps + 1, None
         if isinstance(step, torch.Tensor):
             count_dev = _flat("step", step, tuple(step.shape), torch.int32, dev)
@@ -708,7 +721,7 @@ def adamw_decode(m, m_scale, v, v_scale, dtype=torch.float32, stream=None):
     blocks = (-(-m.numel() // ADAMW_BLOCK),)
     args = (_flat("m", m, shape, torch.int8, dev), _flat("m_scale", m_scale, blocks, torch.float32, dev),
             _flat("v", v, shape, torch.uint8, dev), _flat("v_scale", v_scale, blocks, torch.float32, dev))
-    mo, vo = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+    mo, vo = _new(stream, shape, dtype, dev), _new(stream, shape, dtype, dev)
     _run(lib().vswin_adamw_decode, dev, stream, *args, m.numel(), DTYPES[dtype], mo.data_ptr(), vo.data_ptr())
     return mo, vo
 

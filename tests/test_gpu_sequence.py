@@ -620,3 +620,69 @@ def test_attention_nan_stays_in_its_row(Lq, Lk):
     k[0, Lk - 1, 0, 3] = math.nan
     out, lse = vswin.bias_attention_forward(ins[0], k, *ins[2:], _map(), kv_lens=_i32(Lk, Lk - 1))
     assert out[0, :, 0].isnan().all() and torch.isfinite(out[0, :, 1]).all() and torch.isfinite(out[1]).all()
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("Lq,Lk", [(150, 150), (8, 150), (300, 1500)], ids=str)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attention_unseen_keys_may_hold_anything(d, Lq, Lk, bad):
+    # keys that the causal rule or the bias takes out have the same effect whatever k holds: none
+    ins, _ = _attn_inputs(BF16, 2, Lq, Lk, 2, 1, d)
+    start = _i32(Lk - Lq - 3, Lk - Lq - 40)
+    kw = dict(causal=True, q_start=start)
+    good = vswin.bias_attention_forward(*ins, _map(), **kw)
+    k = ins[1].clone()
+    for b, n in enumerate(start.tolist()):
+        k[b, n + Lq:] = bad
+    got = vswin.bias_attention_forward(ins[0], k, *ins[2:], _map(), **kw)
+    assert torch.equal(got[0], good[0]) and torch.equal(got[1], good[1])
+    # rows before position Lk // 2 do not see that key
+    k = ins[1].clone()
+    k[:, Lk // 2] = bad
+    got = vswin.bias_attention_forward(ins[0], k, *ins[2:], _map(), **kw)
+    for b, n in enumerate(start.tolist()):
+        rows = max(0, min(Lq, Lk // 2 - n))
+        assert torch.equal(got[0][b, :rows], good[0][b, :rows]) and torch.equal(got[1][b, :, :rows], good[1][b, :, :rows])
+    # a map whose bucket 1 (offset 1 alone) is taken out: query i does not see key i + 1
+    every = torch.zeros(7, dtype=torch.int32, device="cuda")
+    every[4] = 1
+    table = torch.tensor([[0.5, -0.5], [-math.inf, -math.inf]], dtype=BF16, device="cuda")
+    q_one = ins[0][:, :1].expand(2, Lq, 2, d)
+    one = dict(q_start=_i32(Lk // 2 - 1, Lk // 2 - 1), q_lens=_i32(1, 1))
+    good = vswin.bias_attention_forward(q_one, *ins[1:3], table, every, **one)
+    got = vswin.bias_attention_forward(q_one, k, ins[2], table, every, **one)
+    assert torch.isfinite(good[0]).all() and torch.equal(got[0], good[0]) and torch.equal(got[1], good[1])
+
+
+def test_results_come_from_the_stream_of_the_call():
+    # memory that the current stream still writes is not handed to a call on another stream
+    ins, do = _attn_inputs(BF16, 1, 256, 256, 2, 2, 64)
+    good = vswin.bias_attention_forward(*ins, _map())
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.empty_like(good[0])
+    at = busy.data_ptr()
+    busy.fill_(1.0)
+    del busy
+    out, lse = vswin.bias_attention_forward(*ins, _map(), stream=s)
+    assert out.data_ptr() != at
+    s.synchronize()
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+
+
+def test_adamw_follows_an_exchanged_weight():
+    n = 1000
+    start = torch.randn(n, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    g = torch.ones(n, device="cuda")
+    a, b = torch.nn.Parameter(start.clone()), torch.nn.Parameter(start.clone())
+    oa, ob = vswin.AdamW([a], **HYPER), vswin.AdamW([b], **HYPER)
+    old = a.data
+    a.data = start.clone()
+    before = old.clone()
+    oa.step([g])
+    ob.step([g])
+    assert torch.equal(a.data, b.data) and torch.equal(old, before) and not torch.equal(a.data, before)
+    a.data = torch.zeros(n + 1, device="cuda")
+    with pytest.raises(ValueError, match=r"params\[0\]"):
+        oa.step([g])
+    torch.cuda.synchronize()
