@@ -114,11 +114,15 @@ int scratch_pool(cudaMemPool_t* out) {
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t pool = nullptr;
+    // (a device's first call may be inside a capture, which forbids the calling thread this in its other modes)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool exchanged = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
     e = cudaMemPoolCreate(&pool, &props);
-    if (e != cudaSuccess) return fail_cuda(e, "cudaMemPoolCreate");
     uint64_t keep = ~0ull;
-    e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
-    if (e != cudaSuccess) return fail_cuda(e, "cudaMemPoolSetAttribute");
+    const cudaError_t e2 = e == cudaSuccess ? cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) : e;
+    if (exchanged) cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return fail_cuda(e, "cudaMemPoolCreate");
+    if (e2 != cudaSuccess) return fail_cuda(e2, "cudaMemPoolSetAttribute");
     g_pool[dev] = pool;
   }
   *out = g_pool[dev];

@@ -3,6 +3,9 @@ of the AdamW step against their float64 definitions. Every output element is hel
 sequence_reference derives for it. Needs a B200."""
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -686,3 +689,35 @@ def test_adamw_follows_an_exchanged_weight():
     with pytest.raises(ValueError, match=r"params\[0\]"):
         oa.step([g])
     torch.cuda.synchronize()
+
+
+FIRST_CALLS = """
+import torch
+from shifted_window_attention_sw_b200 import vswin
+q, k, v, do = (torch.randn(2, 200, 2, 64, device="cuda").bfloat16() for _ in range(4))
+table, one = torch.randn(32, 2, device="cuda").bfloat16(), torch.ones(64, device="cuda").bfloat16()
+bucket_map, p, g = vswin.bucket_map(32, 128), torch.randn(1000, device="cuda"), torch.randn(1000, device="cuda")
+optimizer, count = vswin.AdamW([p]), torch.ones(1, dtype=torch.int32, device="cuda")
+before = p.clone()
+torch.cuda.synchronize()
+
+def step():
+    qn, kn = vswin.qk_norm_forward(q, k, one, one)
+    out, lse = vswin.bias_attention_forward(qn, kn, v, table, bucket_map, causal=True)
+    dq, dk, dv, dt = vswin.bias_attention_backward(qn, kn, v, table, bucket_map, out, lse, do, causal=True)
+    return out, lse, dv, dt, *vswin.qk_norm_backward(q, k, one, one, dq, dk)
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = step()
+    optimizer.step([g], step=count)
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, step())) and not torch.equal(p, before)
+assert vswin.poll_error() == vswin.OK
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    subprocess.run([sys.executable, "-c", FIRST_CALLS], check=True, timeout=300,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
