@@ -12,29 +12,37 @@
 // attn_fwd_kernel: one CTA per 128 query rows of a head, two CTAs per SM. The
 // keys go by in tiles: S = Q K^T on tcgen05 into TMEM (fp32), four softmax warps
 // (TMEM lane = query row) turn it into P (16 bits, written over the scores, the
-// A operand of a TS MMA) and O += P V accumulates in TMEM. D = 32 and 64: tiles
-// of 64 keys, which two groups of four warps take in turns, each with its own
-// score buffer, softmax statistics and sums, joined at the end (sixteen softmax
-// warps per SM). D = 128: one group and tiles of 128 keys, since the MMAs are the
-// bound and read half the shared memory per product of what 64-key tiles do. One
-// warp brings K and V tiles (TMA; a tile in which the keys end goes by cp.async
-// instead, so that nothing behind the lengths is read), one prepares each tile's
-// bias.
+// A operand of a TS MMA) and O += P V accumulates in TMEM. Tiles have 64 keys and
+// two or three score buffers, so that the next scores are there when a tile's P
+// is done. D = 32 and 64: two groups of four warps take the tiles in turns, each
+// with its own softmax statistics and sums, joined at the end (sixteen softmax
+// warps per SM), half a tile in registers at a time. D = 128: TMEM has room for
+// one group's sums; it takes a whole tile at a time (8192 causal tokens, 16 heads
+// over 4: 263 us; half tiles 300; tiles of 128 keys with one score buffer 276;
+// eight warps that share a tile's columns 279). One warp brings K and V tiles
+// (TMA; a tile in which the keys end goes by cp.async instead, so that nothing
+// behind the lengths is read), one prepares each tile's bias.
 //
 // Bias: it depends on j - i alone, so a tile needs 127 + BN values, one line in
 // shared memory that row i reads from entry 127 - i on (consecutive rows,
 // consecutive banks); the causal rule is part of the line (-inf). Tiles of one
 // bucket (all far ones) skip the line: one value for the whole tile.
 //
-// Softmax in one pass over the keys, half a tile in registers at a time: P is
-// formed against the row's reference m, the maximum as it was when it last
-// moved. Only when a score exceeds m by more than kSlack (in log2) does the warp
-// raise m, by a whole number, and rescale what it has by that power of two
-// (without rounding); P is at most 2^kSlack, exact in fp32 sums and finite in 16
-// bits, and o and lse do not depend on m. TMEM columns: scores first, O behind.
+// Softmax in one pass over the keys: P is formed against the row's reference m,
+// the maximum as it was when it last moved. Only when a score exceeds m by more
+// than kSlack (in log2) does the warp raise m, by a whole number, and rescale what
+// it has by that power of two (without rounding); o and lse do not depend on m.
+// P is rounded to the tensors' 16 bits once, as the MMA's operand (at most
+// 2^kSlack, so finite in either type; half a step per key, averaged by the sum),
+// while l sums it unrounded in fp32. TMEM columns: scores first, O behind.
 //
-// Bound: one exponential per visible pair (16 per clock and SM) for D = 32 and
-// 64, the tensor cores for D = 128.
+// Bound: for D = 32 and 64 one exponential per visible pair (16 per clock and
+// SM), for D = 128 the tensor cores; in front of both stands the chain of a
+// softmax warp (wait, TMEM load, maximum, exponentials, store, hand-over: ~1.9 K
+// cycles per 64 keys at D = 128). Measured: 3136 tokens of 4 clips, 12 heads of
+// 32, 170 us of 105 for the exponentials alone; 4096 causal tokens, 24 heads of
+// 64, 92 us (560 TFLOP/s); 8192 causal, 16 heads of 128, 263 us (1.05 PFLOP/s,
+// 0.62 of the measured peak). Without any exponential they take 0.82-0.87 of that.
 #include "bias_attention.cuh"
 #include "bias_attention_split.h"
 
@@ -45,14 +53,12 @@ constexpr int kProducerWarps = 2;
 constexpr int kRing = 4;         // bias lines, and the barriers of scores and P
 constexpr float kSlack = 8.f;
 
-
-
 template <int D>
 struct FwdCfg {
   static constexpr int G = D == 128 ? 1 : 2;     // groups of four softmax warps, each with its own sums O
-  static constexpr int BN = D == 128 ? 128 : 64;  // keys per tile
-  static constexpr int NBUF = D == 128 ? 1 : (D == 64 ? 2 : 3);  // score buffers: what TMEM holds
-  static constexpr int ST = D == 128 ? 1 : 3;     // stages of K and V: two CTAs share 227 KB
+  static constexpr int BN = 64;                   // keys per tile
+  static constexpr int NBUF = D == 32 ? 3 : 2;    // score buffers: what TMEM holds
+  static constexpr int ST = D == 128 ? 2 : 3;     // stages of K and V: two CTAs share 227 KB
   static constexpr int kMmaWarp = 4 * G;
   static constexpr int THREADS = 32 * (4 * G + 1 + kProducerWarps);
   static constexpr int kLineN = 127 + BN;         // offsets in a tile
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
     const float2 c2 = make_float2(c, c);
     float m = 0.f;  // reference of the row (log2), once l > 0
     float l = 0.f;  // sum of P
-    constexpr int kPart = kBn / 2;  // columns in registers at a time (80 or 128 registers)
+    constexpr int kPart = G == 1 ? kBn : kBn / 2;  // columns in registers at a time (120 or 80 registers)
     bool ok = true;
     for (int t = g; t < nt; t += G) {
       ok = warp_wait(&s_full[t % kRing], (t / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up);
@@ -311,6 +317,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
         int r = part(No{}, flat_, cut_, No{});
         if (r == kRedo) r = part(No{}, No{}, Yes{}, Yes{});
         if (r == kFailed) return false;
+        if (kPart == kBn) return true;
         r = part(Yes{}, flat_, cut_, No{});
         if (r == kRedo) r = part(Yes{}, No{}, Yes{}, Yes{});
         return r != kFailed;
