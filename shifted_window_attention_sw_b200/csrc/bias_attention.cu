@@ -406,12 +406,15 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
 // Tiles that are split over the keys: all of them when they fill at most half of
 // the resident CTAs (two per SM); else, when all tiles cost the same, those that
 // would run as a last wave of at most half of them. As many parts as fill one
-// wave, at least 512 keys in each.
+// wave, at least 512 keys in each, or 4096 if they are two (one CTA per SM then
+// runs nearly as fast as two). With and without parts: 4096 causal tokens, 2 heads
+// of 64: 23 and 42 us; 16384, 1 head: 128 and 154; the last wave of 4 x 3136, 12
+// heads of 32: 173 and 184; two parts of 4096, 4 heads: 47 and 44, hence not taken.
 Split forward_split(const BiasAttnArgs& a) {
   const long long tiles = (long long)a.B * a.hq * ((a.Lq + 127) / 128), wave = 2LL * sm_count();
   long long last = 2 * tiles <= wave ? tiles : (a.causal ? 0 : tiles % wave);
   if (2 * last > wave) last = 0;
-  const long long parts = last ? wave / last : 1, most = a.Lk / 512;
+  const long long parts = last ? wave / last : 1, most = a.Lk / (parts > 2 ? 512 : 4096);
   const int n = (int)(parts < most ? parts : (most < 1 ? 1 : most));
   return n > 1 ? Split{n, last * 128, (int)(tiles - last), nullptr, nullptr} : Split{1, 0, 0, nullptr, nullptr};
 }

@@ -13,13 +13,18 @@
 //   dx = r (h - x r mean(h x r)).
 //
 // Both directions are bound by HBM: forward reads x and writes y once, backward
-// reads x and dy and writes dx. Vector path: a row is held by d/16 lanes, each
+// reads x and dy and writes dx. 32 x 3136 tokens, 12 + 12 heads of 32, bf16: 62 us
+// for 309 MB (4.9 TB/s, 0.77 of the measured copy); 4 x 4099 tokens, 16 + 4 heads
+// of 128, fp16: forward 35 us for 168 MB, backward 52 us for 252 MB. What is left
+// is issue (0.5 - 0.6 of the slots) beside the loads' latency. Vector path: a row is held by d/16 lanes, each
 // with 16 channels as eight (a, b) pairs in registers, so that the rotation
 // needs no exchange between lanes. A block takes a few whole tokens at a time,
 // consecutive lanes consecutive heads, and walks the tokens: a lane keeps its
-// head and its gamma, and a position advances by additions alone. Rows whose
-// width, alignment or rotation does not split into 16-byte pieces (the rule is
-// vec_ok) go one row per warp, element by element.
+// head and its gamma, and a position advances by additions alone; the next row's
+// pieces are fetched before the current one is worked on (73 us without). The
+// arithmetic goes two channels per instruction. Rows whose width, alignment or
+// rotation does not split into 16-byte pieces (the rule is vec_ok) go one row per
+// warp, element by element (the 309 MB above from an odd address: 500 us).
 #include "sequence.h"
 
 namespace vswin {
@@ -314,34 +319,40 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
 
 // One row per warp, element by element: any even rot, width up to kMaxD, any
 // alignment and strides.
-template <class T, bool kBackward>
+template <class T, bool kBackward, int kPer>  // kPer: channels per lane
 __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(QkNormArgs a, int qblocks, float* partial) {
   const int w = blockIdx.x < qblocks ? 0 : 1;
   const int block = w ? blockIdx.x - qblocks : blockIdx.x;
   const int blocks = w ? gridDim.x - qblocks : qblocks;
   const int heads = a.heads[w], d = a.d, half = a.rot / 2;
-  const long long rows = (long long)a.B * a.L * heads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* gamma = static_cast<const T*>(a.gamma[w]);
-  constexpr int kPer = kMaxD / 32;
   float sums[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) sums[k] = 0.f;
-  for (long long row = (long long)block * (kThreads / 32) + warp; row < rows;
-       row += (long long)blocks * (kThreads / 32)) {
-    const long long tok = row / heads;
-    const int h = (int)(row - tok * heads), b = (int)(tok / a.L), l = (int)(tok - (long long)b * a.L);
+  // the partner of channel c, its angle, and the sign of its sine term
+  auto pair = [&](int c, int* other, int* angle, float* sign) {
+    *angle = a.interleaved ? c >> 1 : (c < half ? c : c - half);
+    const bool first = a.interleaved ? (c & 1) == 0 : c < half;
+    *other = a.interleaved ? c ^ 1 : (first ? c + half : c - half);
+    *sign = first ? -1.f : 1.f;
+  };
+  // row after row: head, token and sequence advance by additions
+  const int first = block * (kThreads / 32) + warp, step = blocks * (kThreads / 32);
+  const int step_h = step % heads, step_l = step / heads % a.L, step_b = step / heads / a.L;
+  int h = first % heads, l = first / heads % a.L, b = first / heads / a.L;
+  auto next = [&]() {
+    h += step_h;
+    l += step_l;
+    b += step_b;
+    if (h >= heads) h -= heads, ++l;
+    if (l >= a.L) l -= a.L, ++b;
+  };
+  for (; b < a.B; next()) {
     const long long arow = a.rot > 0 ? angle_row(a, b, l) : 0;
     const T* xp = static_cast<const T*>(a.x[w].p) + a.x[w].at(b, l, h);
     const T* yp = static_cast<const T*>(a.y[w].p) + a.y[w].at(b, l, h);
     float x[kPer], part[kPer], ss = 0.f;  // own channel, and its partner's of the rotation
-    // the partner of channel c, its angle, and the sign of its sine term
-    auto pair = [&](int c, int* other, int* angle, float* sign) {
-      *angle = a.interleaved ? c >> 1 : (c < half ? c : c - half);
-      const bool first = a.interleaved ? (c & 1) == 0 : c < half;
-      *other = a.interleaved ? c ^ 1 : (first ? c + half : c - half);
-      *sign = first ? -1.f : 1.f;
-    };
     float g[kPer], gpart[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -475,7 +486,7 @@ void plan(const QkNormArgs& a, bool* vec, int* G, int* nq, int* nk) {
     const int groups = kThreads / *G, per = groups / a.heads[w] > 0 ? groups / a.heads[w] : 1;
     need[w] = *vec ? (tokens + per - 1) / per : (tokens * a.heads[w] + groups - 1) / groups;
   }
-  grid_of(a, need, kBackward ? 2 : 3, nq, nk);
+  grid_of(a, need, !*vec ? 8 : (kBackward ? 2 : 3), nq, nk);
 }
 
 template <class T, bool kBackward, bool kInter>
@@ -499,8 +510,14 @@ cudaError_t launch(const QkNormArgs& a, float* partial, cudaStream_t st) {
   plan<T, kBackward>(a, &vec, &G, &nq, &nk);
   const int grid = nq + nk;
   prof_begin(kKindOther, st);
-  if (!vec)
-    qk_norm_any_kernel<T, kBackward><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  if (!vec && a.d <= 32)
+    qk_norm_any_kernel<T, kBackward, 1><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (!vec && a.d <= 64)
+    qk_norm_any_kernel<T, kBackward, 2><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (!vec && a.d <= 128)
+    qk_norm_any_kernel<T, kBackward, 4><<<grid, kThreads, 0, st>>>(a, nq, partial);
+  else if (!vec)
+    qk_norm_any_kernel<T, kBackward, 8><<<grid, kThreads, 0, st>>>(a, nq, partial);
   else if (a.interleaved && a.rot)
     launch_vec<T, kBackward, true>(a, G, grid, nq, partial, st);
   else

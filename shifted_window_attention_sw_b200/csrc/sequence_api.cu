@@ -71,8 +71,9 @@ int check_qk_norm(int dtype, int B, int L, int hq, int hk, int d, const vswin_he
     return fail(VSWIN_ERR_INVALID_ARG, "sizes must be positive (B=%d L=%d heads=%d,%d d=%d)", B, L, hq, hk, d);
   if (d > 256) return fail(VSWIN_ERR_UNSUPPORTED, "head width %d: the norm supports up to 256", d);
   const long long most = (long long)B * L;
-  if (most > (1LL << 31) - (1LL << 20) || most * hq > (1LL << 40) || most * hk > (1LL << 40))
-    return fail(VSWIN_ERR_UNSUPPORTED, "B * L exceeds 2^31 - 2^20 or rows exceed 2^40");
+  if (most > (1LL << 31) - (1LL << 20) || hq > (1 << 20) || hk > (1 << 20) || most * hq > (1LL << 40) ||
+      most * hk > (1LL << 40))
+    return fail(VSWIN_ERR_UNSUPPORTED, "B * L exceeds 2^31 - 2^20, heads 2^20 or rows 2^40");
   if (!(eps >= 0.f) || !std::isfinite(eps))
     return fail(VSWIN_ERR_INVALID_ARG, "eps must be finite and >= 0 (got %g)", (double)eps);
   const int es = elem_bytes(dtype);

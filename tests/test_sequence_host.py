@@ -75,6 +75,12 @@ def test_norm_unsupported_width(L):
     _refused(L, _norm(L, d=257), vswin.ERR_UNSUPPORTED, before)
 
 
+@pytest.mark.parametrize("kw", [dict(hq=(1 << 20) + 1), dict(hk=(1 << 20) + 1), dict(B=1 << 16, Lt=1 << 15)], ids=str)
+def test_norm_unsupported_sizes(L, kw):
+    before = vswin.launch_count()
+    _refused(L, _norm(L, **kw), vswin.ERR_UNSUPPORTED, before)
+
+
 def _attn(L, dtype=0, B=2, Lq=8, Lk=8, hq=4, hk=2, d=64, q=None, k=None, v=None, scale=0.125, table=4, bmap=5, buckets=32,
           D=128, vis=None, out=None, lse=7, back=None):
     q = _view(1, Lq, max(hq, 1), d) if q is None else q
