@@ -445,10 +445,10 @@ def _heads(name, t, shape, dtype, device):
     """View of a (B, L, heads, d) tensor; its channels have to be contiguous."""
     if t.dtype is not dtype or t.shape != shape or t.device != device:
         _refuse(name, t, shape, dtype, device)
-    sb, st, sh, sd = t.stride()
-    if sd != 1 and shape[3] > 1:
+    strides = t.stride()
+    if strides[3] != 1 and shape[3] > 1:
         _refuse(name, t, shape, dtype, device)
-    return _Heads(t.data_ptr(), sb, st, sh)
+    return _Heads(t.data_ptr(), *strides[:3])
 
 
 def _flat(name, t, shape, dtype, device):
@@ -478,38 +478,41 @@ def _run(fn, dev, stream, *args):
         raise VswinError(status, last_error())
 
 
-def _new(stream, like, shape, dtype):
-    """Contiguous memory for a result on the device of a tensor, from the stream that the call runs on."""
+def _new(stream, like, shape=None, dtype=None):
+    """Contiguous memory for a result, of a tensor's shape and type or of others on its device, from the stream
+    that the call runs on."""
     # (the cheapest of torch's ways: 1.4 us for a shape like the tensor's, 1.9 for another, 2.4 for torch.empty)
     if stream is not None:
         with torch.cuda.stream(stream):
-            return like.new_empty(shape, dtype=dtype)
-    if like.shape == shape and like.dtype is dtype:
+            return _new(None, like, shape, dtype)
+    if shape is None:
         return torch.empty_like(like, memory_format=torch.contiguous_format)
     return like.new_empty(shape, dtype=dtype)
 
 
 def _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved):
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(q.shape)} and {tuple(k.shape)}")
-    if q.dtype not in DTYPES:
-        raise TypeError(f"q must be one of {list(DTYPES)}, got {q.dtype}")
-    B, L, hq, d = q.shape
-    hk, dt, dev = k.shape[2], q.dtype, q.device
+    shape, k_shape = q.shape, k.shape
+    if len(shape) != 4 or len(k_shape) != 4:
+        raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(shape)} and {tuple(k_shape)}")
+    B, L, hq, d = shape
+    hk, dt, dev = k_shape[2], q.dtype, q.device
+    code = DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"q must be one of {list(DTYPES)}, got {dt}")
     if not q.is_cuda:
-        _refuse("q", q, q.shape, dt, dev)
+        _refuse("q", q, shape, dt, dev)
     rot = None
     if cos is not None or sin is not None:
         if cos is None or sin is None or cos.dim() != 2:
             raise ValueError("cos and sin must both be (rows, dim / 2)")
-        shape = tuple(cos.shape)
-        rot = _Rotation(_flat("cos", cos, shape, torch.float32, dev), _flat("sin", sin, shape, torch.float32, dev),
-                        shape[0], 2 * shape[1], 1 if interleaved else 0,
+        angles = tuple(cos.shape)
+        rot = _Rotation(_flat("cos", cos, angles, torch.float32, dev), _flat("sin", sin, angles, torch.float32, dev),
+                        angles[0], 2 * angles[1], 1 if interleaved else 0,
                         _flat("positions", positions, (B, L), torch.int32, dev))
     elif positions is not None:
         raise ValueError("positions need cos and sin")
-    views = (_heads("q", q, (B, L, hq, d), dt, dev), _heads("k", k, (B, L, hk, d), dt, dev))
-    return (B, L, hq, hk, d, dt, dev), [DTYPES[dt], B, L, hq, hk, d, *views,
+    return (B, L, hq, hk, d, dt, dev), [code, B, L, hq, hk, d, _heads("q", q, shape, dt, dev),
+                                        _heads("k", k, (B, L, hk, d), dt, dev),
                                         _flat("gamma_q", gamma_q, (d,), dt, dev),
                                         _flat("gamma_k", gamma_k, (d,), dt, dev), float(eps), rot]
 
@@ -521,8 +524,8 @@ def qk_norm_forward(q, k, gamma_q, gamma_k, eps=1e-6, cos=None, sin=None, positi
     them) of the float32 tables cos and sin, in one pass; bf16, fp16 or fp32. Views with contiguous channels
     are taken as they are. ``q_out`` may be ``q`` and ``k_out`` ``k``. Returns (q_out, k_out)."""
     (B, L, hq, hk, d, dt, dev), args = _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
-    q_out = _new(stream, q, (B, L, hq, d), dt) if q_out is None else q_out
-    k_out = _new(stream, k, (B, L, hk, d), dt) if k_out is None else k_out
+    q_out = _new(stream, q) if q_out is None else q_out
+    k_out = _new(stream, k) if k_out is None else k_out
     _run(lib().vswin_qk_norm_forward, dev, stream, *args, _heads("q_out", q_out, (B, L, hq, d), dt, dev),
          _heads("k_out", k_out, (B, L, hk, d), dt, dev))
     return q_out, k_out
@@ -533,8 +536,8 @@ def qk_norm_backward(q, k, gamma_q, gamma_k, dq_out, dk_out, eps=1e-6, cos=None,
     """Gradients (dq, dk in the type of q; dgamma_q, dgamma_k float32) of qk_norm_forward for the output
     gradients ``dq_out`` and ``dk_out``. ``dq`` and ``dk`` may be given, e.g. as slices of one buffer."""
     (B, L, hq, hk, d, dt, dev), args = _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
-    dq = _new(stream, q, (B, L, hq, d), dt) if dq is None else dq
-    dk = _new(stream, k, (B, L, hk, d), dt) if dk is None else dk
+    dq = _new(stream, q) if dq is None else dq
+    dk = _new(stream, k) if dk is None else dk
     dgamma = _new(stream, q, (2, d), torch.float32)
     at = dgamma.data_ptr()
     _run(lib().vswin_qk_norm_backward, dev, stream, *args, _heads("dq_out", dq_out, (B, L, hq, d), dt, dev),
@@ -553,27 +556,27 @@ def bucket_map(buckets, max_distance, bidirectional=True, device="cuda"):
 
 
 def _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens, kv_lens, q_start):
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(q.shape)} and {tuple(k.shape)}")
-    if q.dtype not in DTYPES:
-        raise TypeError(f"q must be torch.bfloat16 or torch.float16, got {q.dtype}")
-    B, Lq, hq, d = q.shape
-    Lk, hk = k.shape[1:3]
-    dt, dev = q.dtype, q.device
+    shape, k_shape, table_shape, map_shape = q.shape, k.shape, table.shape, bucket_map.shape
+    if len(shape) != 4 or len(k_shape) != 4:
+        raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(shape)} and {tuple(k_shape)}")
+    B, Lq, hq, d = shape
+    Lk, hk, dt, dev = k_shape[1], k_shape[2], q.dtype, q.device
+    code = DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"q must be torch.bfloat16 or torch.float16, got {dt}")
     if not q.is_cuda:
-        _refuse("q", q, q.shape, dt, dev)
-    if table.dim() != 2 or bucket_map.dim() != 1 or bucket_map.shape[0] % 2 == 0:
+        _refuse("q", q, shape, dt, dev)
+    if len(table_shape) != 2 or len(map_shape) != 1 or map_shape[0] % 2 == 0:
         raise ValueError("table must be (buckets, heads of q) and bucket_map (2 * max_distance + 1,), got "
-                         f"{tuple(table.shape)} and {tuple(bucket_map.shape)}")
-    buckets, D = table.shape[0], bucket_map.shape[0] // 2
-    views = (_heads("q", q, (B, Lq, hq, d), dt, dev), _heads("k", k, (B, Lk, hk, d), dt, dev),
-             _heads("v", v, (B, Lk, hk, d), dt, dev))
+                         f"{tuple(table_shape)} and {tuple(map_shape)}")
+    buckets, D, ks = table_shape[0], map_shape[0] // 2, (B, Lk, hk, d)
+    views = (_heads("q", q, shape, dt, dev), _heads("k", k, ks, dt, dev), _heads("v", v, ks, dt, dev))
     bias = _BucketBias(_flat("table", table, (buckets, hq), dt, dev),
                        _flat("bucket_map", bucket_map, (2 * D + 1,), torch.int32, dev), buckets, D)
     vis = _Visibility(_flat("q_lens", q_lens, (B,), torch.int32, dev), _flat("kv_lens", kv_lens, (B,), torch.int32, dev),
                       _flat("q_start", q_start, (B,), torch.int32, dev), 1 if causal else 0)
     scale = d ** -0.5 if scale is None else float(scale)
-    return (B, Lq, Lk, hq, hk, d, dt, dev), [DTYPES[dt], B, Lq, Lk, hq, hk, d, *views, scale, bias, vis]
+    return (B, Lq, Lk, hq, hk, d, dt, dev), [code, B, Lq, Lk, hq, hk, d, *views, scale, bias, vis]
 
 
 def bias_attention_forward(q, k, v, table, bucket_map, scale=None, causal=False, q_lens=None, kv_lens=None,
@@ -585,7 +588,7 @@ def bias_attention_forward(q, k, v, table, bucket_map, scale=None, causal=False,
     cache: Lq = 1, q_start = kv_lens - 1. Returns (out, lse), lse float32 (B, hq, Lq)."""
     (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
                                                                  kv_lens, q_start)
-    out = _new(stream, q, (B, Lq, hq, d), dt) if out is None else out
+    out = _new(stream, q) if out is None else out
     lse = _new(stream, q, (B, hq, Lq), torch.float32) if lse is None else lse
     _run(lib().vswin_bias_attention_forward, dev, stream, *args, _heads("out", out, (B, Lq, hq, d), dt, dev),
          _flat("lse", lse, (B, hq, Lq), torch.float32, dev))
@@ -599,8 +602,8 @@ def bias_attention_backward(q, k, v, table, bucket_map, out, lse, dout, scale=No
     (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
                                                                  kv_lens, q_start)
     qs, ks = (B, Lq, hq, d), (B, Lk, hk, d)
-    dq, dk, dv = (_new(stream, like, s, dt) if t is None else t for t, like, s in ((dq, q, qs), (dk, k, ks), (dv, k, ks)))
-    dtable = _new(stream, table, table.shape, dt)
+    dq, dk, dv = (_new(stream, like) if t is None else t for t, like in ((dq, q), (dk, k), (dv, v)))
+    dtable = _new(stream, table)
     _run(lib().vswin_bias_attention_backward, dev, stream, *args, _heads("out", out, qs, dt, dev),
          _flat("lse", lse, (B, hq, Lq), torch.float32, dev), _heads("dout", dout, qs, dt, dev),
          _heads("dq", dq, qs, dt, dev), _heads("dk", dk, ks, dt, dev), _heads("dv", dv, ks, dt, dev), dtable.data_ptr())
