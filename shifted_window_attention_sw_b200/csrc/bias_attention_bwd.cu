@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
   using Line = typename C::Line;
   constexpr int G = C::G, ST = C::ST;
   constexpr int kMmaWarp = C::kWarps;
+  let_next_start();
   extern __shared__ __align__(1024) uint8_t smem[];
   const BiasAttnArgs& a = args.a;
   Line* lines = reinterpret_cast<Line*>(smem + C::OFF_LINE);
@@ -145,6 +146,8 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const uint32_t sf = smem_u32(smem + C::OFF_F), sm = smem_u32(smem + C::OFF_M);
+  // the other pass, whose D this one reads (before any bounded wait; and the table's sums count on both having ended)
+  if (kKeys) after_previous();
 
   if (warp > kMmaWarp) {
     // ------------------------------------------------------------ producers: tiles; bias lines and columns
@@ -486,6 +489,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
 // block, eight runs of shares side by side.
 template <class T>
 __global__ void __launch_bounds__(256) attn_dtable_kernel(const float* dtab, int shares, int buckets, int hq, T* out) {
+  after_previous();
   __shared__ float s[8][33];
   const int h = blockIdx.x, lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int k = blockIdx.y * 32 + lane;
@@ -519,10 +523,15 @@ cudaError_t pass(BwdArgs& args, cudaStream_t st) {
   map(&args.m2, kKeys ? a.dout : a.v, !kKeys, kBn);
   const long long grid = (long long)a.B * (kKeys ? a.hk : a.hq) * (((kKeys ? a.Lk : a.Lq) + 127) / 128);
   prof_begin(kKindAttnBwd, st);
-  attn_bwd_kernel<T, D, kKeys><<<(unsigned)grid, C::THREADS, smem, st>>>(args);
+  if (kKeys) {
+    e = launch_after(attn_bwd_kernel<T, D, kKeys>, dim3((unsigned)grid), C::THREADS, smem, st, args);
+  } else {
+    attn_bwd_kernel<T, D, kKeys><<<(unsigned)grid, C::THREADS, smem, st>>>(args);
+    e = cudaGetLastError();
+  }
   prof_end(kKindAttnBwd, st);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 size_t delta_bytes(const BiasAttnArgs& a) { return ((size_t)a.B * a.hq * a.Lq * 4 + 255) / 256 * 256; }
@@ -537,11 +546,11 @@ cudaError_t backward(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
   if (e == cudaSuccess) e = pass<T, D, true>(args, st);
   if (e != cudaSuccess) return e;
   prof_begin(kKindOther, st);
-  attn_dtable_kernel<T><<<dim3(a.hq, (a.buckets + 31) / 32), 256, 0, st>>>(args.dtab, a.B * ((a.Lq + 127) / 128), a.buckets,
-                                                                          a.hq, static_cast<T*>(a.dtable));
+  e = launch_after(attn_dtable_kernel<T>, dim3(a.hq, (a.buckets + 31) / 32), 256, 0, st, args.dtab, a.B * ((a.Lq + 127) / 128),
+                   a.buckets, a.hq, static_cast<T*>(a.dtable));
   prof_end(kKindOther, st);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 template <class T>

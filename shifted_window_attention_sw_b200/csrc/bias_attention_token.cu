@@ -61,6 +61,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(32 * kWarps, TokCfg<D>::CTAS)
     attn_token_kernel(const __grid_constant__ BiasAttnArgs a, Split sp, int blocks) {
   using C = TokCfg<D>;
+  if (sp.n > 1) let_next_start();
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qc = lane & 3;
   const int group = a.hq / a.hk, rows = a.Lq * group;
@@ -272,6 +273,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
+  after_previous();
   int i, h, b;
   if (sp.first < 0) {
     i = (int)(r % a.Lq), h = (int)(r / a.Lq % a.hq), b = (int)(r / a.Lq / a.hq);
@@ -349,10 +351,10 @@ cudaError_t token_d(const BiasAttnArgs& a, void* scratch, cudaStream_t st) {
 template <class T, int D>
 cudaError_t launch_attention_join(const BiasAttnArgs& a, const Split& sp, cudaStream_t st) {
   prof_begin(kKindOther, st);
-  attn_join_kernel<T, D><<<(unsigned)((sp.rows + 3) / 4), 128, 0, st>>>(a, sp);
+  const cudaError_t e = launch_after(attn_join_kernel<T, D>, dim3((unsigned)((sp.rows + 3) / 4)), 128, 0, st, a, sp);
   prof_end(kKindOther, st);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 template cudaError_t launch_attention_join<__nv_bfloat16, 32>(const BiasAttnArgs&, const Split&, cudaStream_t);
 template cudaError_t launch_attention_join<__nv_bfloat16, 64>(const BiasAttnArgs&, const Split&, cudaStream_t);

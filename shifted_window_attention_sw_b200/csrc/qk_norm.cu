@@ -160,6 +160,7 @@ __host__ __device__ __forceinline__ int tokens_per_step(int heads) {
 template <class T, int G, bool kBackward, bool kInter>
 __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
     qk_norm_vec_kernel(const __grid_constant__ QkNormArgs a, int qblocks, float* partial) {
+  if (kBackward) let_next_start();
   const int w = blockIdx.x < qblocks ? 0 : 1;
   const int block = w ? blockIdx.x - qblocks : blockIdx.x;
   const int blocks = w ? gridDim.x - qblocks : qblocks;
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3)
 // alignment and strides.
 template <class T, bool kBackward, int kPer>  // kPer: channels per lane
 __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(QkNormArgs a, int qblocks, float* partial) {
+  if (kBackward) let_next_start();
   const int w = blockIdx.x < qblocks ? 0 : 1;
   const int block = w ? blockIdx.x - qblocks : blockIdx.x;
   const int blocks = w ? gridDim.x - qblocks : qblocks;
@@ -422,6 +424,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(QkNormArgs a, int
 // runs of shares side by side.
 __global__ void __launch_bounds__(1024) qk_norm_dgamma_kernel(QkNormArgs a, int qblocks, int blocks,
                                                              const float* partial) {
+  after_previous();
   __shared__ float s[32][33];
   const int w = blockIdx.y, lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -527,10 +530,10 @@ cudaError_t launch(const QkNormArgs& a, float* partial, cudaStream_t st) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !kBackward) return e;
   prof_begin(kKindOther, st);
-  qk_norm_dgamma_kernel<<<dim3((a.d + 31) / 32, 2), 1024, 0, st>>>(a, nq, grid, partial);
+  e = launch_after(qk_norm_dgamma_kernel, dim3((a.d + 31) / 32, 2), 1024, 0, st, a, nq, grid, partial);
   prof_end(kKindOther, st);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
