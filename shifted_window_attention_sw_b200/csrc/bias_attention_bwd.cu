@@ -15,9 +15,10 @@
 // forward (the seven products that both need take 107 us at the measured peak);
 // 8 x 577 tokens, 6 heads: 29 + 25 us. Tensor cores 0.27 and 0.32 busy, special functions
 // 0.36 and 0.32, issue 0.42: bound by the chain scores - P and dS - sums of a CTA,
-// which the other CTA of the SM covers in part. Tried: three groups of warps in one
-// CTA (slower, one warp issues for all), columns' (lse, D) fetched a tile earlier
-// (no change).
+// which the other CTA of the SM covers in part. Tried: one CTA per SM with two
+// groups of warps and three score buffers (163 instead of 145 us for the first
+// pass) or with three groups (slower, too: one warp issues for all), columns'
+// (lse, D) fetched a tile earlier (no change).
 //
 // P and dS are rounded to the tensors' 16 bits once, as operands of the sums; D
 // comes from the 16-bit out. dtable sums the unrounded dS in fp32.
