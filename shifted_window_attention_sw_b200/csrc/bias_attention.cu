@@ -33,8 +33,8 @@
 // than kSlack (in log2) does the warp raise m, by a whole number, and rescale what
 // it has by that power of two (without rounding); o and lse do not depend on m.
 // P is rounded to the tensors' 16 bits once, as the MMA's operand (at most
-// 2^kSlack, so finite in either type; half a step per key, averaged by the sum),
-// while l sums it unrounded in fp32. TMEM columns: scores first, O behind.
+// 2^kSlack, so finite in either type; half a step per key, or 2^-25 in fp16 where
+// that is more), while l sums it unrounded in fp32. TMEM columns: scores first, O behind.
 //
 // Bound: for D = 32 and 64 one exponential per visible pair (16 per clock and
 // SM), for D = 128 the tensor cores; in front of both stands the chain of a
@@ -283,8 +283,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
               tmem_st8(buf + e, r);
             }
           }
-          if (t >= G) {  // (the group's sums so far: complete before these scores were, or waited for)
-            if (G == 1 && !warp_wait(&o_done[(t - 1) % kRing], ((t - 1) / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up)) return kFailed;
+          if (t >= G) {
+            // the group's sums so far: these scores came after them if they took the buffer of its last tile
+            if (NBUF != G && !warp_wait(&o_done[(t - G) % kRing], ((t - G) / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up))
+              return kFailed;
             tc_fence_after();
 #pragma unroll
             for (int e = 0; e < D; e += 8) {

@@ -721,3 +721,13 @@ assert vswin.poll_error() == vswin.OK
 def test_first_calls_of_a_process_may_be_captured():
     subprocess.run([sys.executable, "-c", FIRST_CALLS], check=True, timeout=300,
                    cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("dtype,Lq,Lk", [(BF16, 130, 2100), (FP16, 511, 700), (BF16, 4, 2100)], ids=str)
+def test_attention_scores_that_grow_along_the_keys(dtype, Lq, Lk, d, causal):
+    # every tile raises the running maximum of most rows, so that the sums so far are rescaled again and again
+    ins, do = _attn_inputs(dtype, 2, Lq, Lk, 4, 2, d)
+    ins[1] = (ins[1].float() * torch.linspace(0.1, 1.0, Lk, device="cuda").view(1, Lk, 1, 1)).to(dtype)
+    _attn_check(ins, _map(), do, scale=0.5, causal=causal, q_start=_i32(Lk - Lq, Lk - Lq), backward=causal)
