@@ -228,7 +228,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       const int live = nk - (t0 + t) * kBn;  // columns of the tile that are keys
       // one part of the tile: of one bucket or not, with keys missing or not; kRedo when a score is NaN, then again
       // with `careful`, where NaN or infinity in a key that the bias or the causal rule takes out does not count
-      enum { kFailed, kDone, kRedo };
+      enum { kDone, kRedo, kWait };
+      // the group's sums so far are complete: these scores came after them if they took the buffer of its last tile;
+      // else a part that has to rescale them says kWait and goes again
+      bool settled = NBUF == G || t < G;
       auto part = [&](auto second_, auto flat_, auto cut_, auto careful_) -> int {
         constexpr int c0 = decltype(second_)::value ? kPart : 0;
         constexpr bool kFlat = decltype(flat_)::value, kCut = decltype(cut_)::value, kCareful = decltype(careful_)::value;
@@ -262,6 +265,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
         // (unordered comparisons: a NaN enters, too)
         if (__any_sync(0xffffffffu, l == 0.f ? top != -INFINITY : !(top <= kSlack))) {
           if (!kCareful && __any_sync(0xffffffffu, top != top)) return kRedo;
+          if (!settled) return kWait;
           const bool move = l == 0.f ? top > -INFINITY : top > kSlack;
           // by whole powers of two, so that what is there already is rescaled without rounding
           const float step = move ? ceilf(top) : 0.f;
@@ -283,10 +287,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
               tmem_st8(buf + e, r);
             }
           }
-          if (t >= G) {
-            // the group's sums so far: these scores came after them if they took the buffer of its last tile
-            if (NBUF != G && !warp_wait(&o_done[(t - G) % kRing], ((t - G) / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up))
-              return kFailed;
+          if (t >= G) {  // the sums so far
             tc_fence_after();
 #pragma unroll
             for (int e = 0; e < D; e += 8) {
@@ -316,14 +317,22 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
       };
       using Yes = std::true_type;
       using No = std::false_type;
+      auto whole = [&](auto second_, auto flat_, auto cut_) {
+        int r;
+        while ((r = part(second_, flat_, cut_, No{})) == kWait) {
+          settled = warp_wait(&o_done[(t - G) % kRing], ((t - G) / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up);
+          if (!settled) return false;
+        }
+        if (r == kRedo) {
+          if (!settled && !warp_wait(&o_done[(t - G) % kRing], ((t - G) / kRing) & 1, a.ctx, kErrAttnSoftmax, gave_up))
+            return false;
+          settled = true;
+          part(second_, No{}, Yes{}, Yes{});
+        }
+        return true;
+      };
       auto tile = [&](auto flat_, auto cut_) {
-        int r = part(No{}, flat_, cut_, No{});
-        if (r == kRedo) r = part(No{}, No{}, Yes{}, Yes{});
-        if (r == kFailed) return false;
-        if (kPart == kBn) return true;
-        r = part(Yes{}, flat_, cut_, No{});
-        if (r == kRedo) r = part(Yes{}, No{}, Yes{}, Yes{});
-        return r != kFailed;
+        return whole(No{}, flat_, cut_) && (kPart == kBn || whole(Yes{}, flat_, cut_));
       };
       if (live >= kBn)
         ok = flat ? tile(Yes{}, No{}) : tile(No{}, No{});
