@@ -192,6 +192,12 @@ __device__ __forceinline__ float warp_max_nan(float x) {
   asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
+// The larger of two, NaN when one of them is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
 __device__ __forceinline__ float rcp_fast(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -267,11 +273,16 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
           root[k] = sqrt_flush(v2.x);
           root[k + 1] = sqrt_flush(v2.y);
           const float2 d = __ffma2_rn(make_float2(root[k], root[k + 1]), both(inv_bc2), both(h.eps));
-          const float2 inv = make_float2(rcp_fast(fmaxf(d.x, 0x1p-66f)), rcp_fast(fmaxf(d.y, 0x1p-66f)));
+          // (a NaN v has to reach the weight)
+          const float2 inv = make_float2(rcp_fast(max_nan(d.x, 0x1p-66f)), rcp_fast(max_nan(d.y, 0x1p-66f)));
           const float2 p2 = __ffma2_rn(__fmul2_rn(both(-step_size), m2), inv, __fmul2_rn(both(t.keep), make_float2(p[k], p[k + 1])));
           m[k] = m2.x, m[k + 1] = m2.y, v[k] = v2.x, v[k + 1] = v2.y, p[k] = p2.x, p[k + 1] = p2.y;
         }
-        // (elements behind the tensor are zero here)
+        if (i + 8 > n) {  // elements behind the tensor (their code 0 of an infinite or NaN scale is NaN)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i + k >= n) m[k] = v[k] = 0.f;
+        }
         const float top_m = warp_max_nan(max3_nan(max3_nan(m[0], m[1], m[2]), max3_nan(m[3], m[4], m[5]), max3_nan(m[6], m[7], 0.f)));
         const float top_v = warp_max_nan(max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), max3_nan(v[6], v[7], 0.f)));
         // code = 127 sqrt(|m| / s), 255 sqrt(sqrt(v) / sqrt(s)); blocks below 2^-100 have no use for codes, and 1 / s no overflow

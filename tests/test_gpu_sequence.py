@@ -731,3 +731,56 @@ def test_attention_scores_that_grow_along_the_keys(dtype, Lq, Lk, d, causal):
     ins, do = _attn_inputs(dtype, 2, Lq, Lk, 4, 2, d)
     ins[1] = (ins[1].float() * torch.linspace(0.1, 1.0, Lk, device="cuda").view(1, Lk, 1, 1)).to(dtype)
     _attn_check(ins, _map(), do, scale=0.5, causal=causal, q_start=_i32(Lk - Lq, Lk - Lq), backward=causal)
+
+
+def _adamw_8_definition(opt, p, g, i, wd, step, gs=1.0, w=None):
+    """(p, m, v) of tensor i after a step from the codes that the object holds, float64, and the scales' blocks."""
+    up = lambda s: s.double().repeat_interleave(256)[:p.numel()]  # noqa: E731
+    c, d = opt.m[i].double().view(-1), opt.v[i].double().view(-1)
+    m0, v0 = up(opt.m_scale[i]) * c * c.abs() / 127**2, up(opt.v_scale[i]) * (d / 255) ** 4
+    w = p if w is None else w
+    return ref.adamw(w.double().view(-1), gs * g.double().view(-1), m0, v0, HYPER["lr"], *HYPER["betas"], HYPER["eps"], wd, step)
+
+
+def _block_max(x, n):
+    return torch.nn.functional.pad(x, (0, -n % 256)).view(-1, 256).abs().amax(1)
+
+
+@pytest.mark.parametrize("codes_from", [0, 1])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_adamw_8_second_moments_that_are_not_finite(offset, codes_from):
+    # scales of infinity and NaN beside finite first moments: v = scale (c / 255)^4 is infinite (no step), or NaN
+    # (c = 0 of an infinite scale, every c of NaN), and then so is the weight; the last block is a partial one
+    n = 900
+    p, g = _adamw_lists([n], [F32], [F32], offset=offset)
+    at = torch.arange(n, device="cuda")
+    m, v = (at % 255 - 127).to(torch.int8), (codes_from + at % (256 - codes_from)).to(torch.uint8)
+    ms = torch.full((4,), 1e-3, device="cuda")
+    vs = torch.tensor([math.inf, math.nan, 1e-4, math.inf], device="cuda")
+    opt = vswin.AdamW(p, bits=8, weight_decay=0.1, moments=([m], [v]), scales=([ms], [vs]), **HYPER)
+    for step in (4, 5):
+        w, mw, vw = _adamw_8_definition(opt, p[0], g[0], 0, 0.1, step)
+        opt.step(g, step=step)
+        _adamw_bounds(w, p[0], F32)
+        sm, sv = _block_max(mw, n), _block_max(vw, n)
+        _close("m_scale", opt.m_scale[0], sm, 1e-6 * sm)
+        _close("v_scale", opt.v_scale[0], sv, torch.where(sv.isfinite(), 1e-6 * sv, 0.0))
+
+
+def test_adamw_8_gradient_whose_square_overflows():
+    # one gradient of 1e21: its v is infinite in fp32 and so is its block's scale, m stays finite. From then on the
+    # block's weights stand still or are NaN, none is thrown far away; the other blocks go on
+    n = 600
+    p, g = _adamw_lists([n], [F32], [F32])
+    opt = vswin.AdamW(p, bits=8, weight_decay=0.0, **HYPER)
+    g[0][550] = 1e21
+    opt.step(g)
+    g[0][550] = 1e-2
+    for step in (2, 3, 4):
+        w, _, _ = _adamw_8_definition(opt, p[0], g[0], 0, 0.0, step)
+        before = p[0].clone()
+        opt.step(g)
+        _adamw_bounds(w, p[0], F32)
+        moved = (p[0] - before).abs()
+        assert torch.isfinite(p[0][:512]).all()
+        assert ((moved[512:] == 0) | moved[512:].isnan()).all()
