@@ -368,8 +368,8 @@ int vswin_bucket_map(int buckets, int max_distance, int bidirectional, int* map)
  * [2 max_distance + 1] on the device (vswin_bucket_map's or any other), offsets
  * beyond max_distance read its ends. buckets up to 512, max_distance up to
  * 2^20. A bias at or below -1e30 takes the key out of the softmax. A map entry
- * outside [0, buckets) counts as bias 0 and is reported by vswin_poll_error
- * (VSWIN_ERR_BOUNDS). */
+ * outside [0, buckets) counts as bias 0, belongs to no row of the table's
+ * gradient and is reported by vswin_poll_error (VSWIN_ERR_BOUNDS). */
 typedef struct {
   const void* table;
   const int* map;

@@ -20,6 +20,10 @@ namespace vswin {
 // A bias at or below this takes its key out of the softmax, as -inf does (so
 // that the lowest value of a type works as a mask).
 constexpr float kExclude = -1e30f;
+// What a line's buckets hold for an offset whose map entry lies outside the table: its bias is 0 and it belongs to no
+// row of the table's gradient.
+constexpr int kNoBucket = 0xffff;
+static_assert(kMaxBuckets <= kNoBucket, "no bucket of a table");
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -49,14 +53,14 @@ __device__ __forceinline__ SeqLens seq_lens(const BiasAttnArgs& a, int b) {
 
 // Bias of head h at offset `rel` = key - position of the query, -inf for a key
 // that it takes out; a bucket outside the table is recorded in the error word
-// and its bias is 0 (bucket 0 for the gradient).
+// and its bias is 0 (kNoBucket for the gradient).
 template <class T>
 __device__ __forceinline__ float bias_of(const BiasAttnArgs& a, int rel, int h, int* bucket = nullptr) {
   const int at = (rel < -a.D ? -a.D : (rel > a.D ? a.D : rel)) + a.D;
   int k = __ldg(a.map + at);
   if (k < 0 || k >= a.buckets) {
     atomicCAS(a.ctx.err, 0, kErrBounds);
-    if (bucket) *bucket = 0;
+    if (bucket) *bucket = kNoBucket;
     return 0.f;
   }
   if (bucket) *bucket = k;
@@ -336,7 +340,7 @@ struct LineWriter {
       for (int t = 0; t < kPer; ++t) {
         const bool in = (unsigned)k[t] < (unsigned)a.buckets;
         bad = bad || !in;
-        k[t] = in ? k[t] : 0;
+        k[t] = in ? k[t] : kNoBucket;
         v[t] = in ? to_f(static_cast<const T*>(a.table)[(long long)k[t] * a.hq + h]) : 0.f;
       }
       if (bad) atomicCAS(a.ctx.err, 0, kErrBounds);

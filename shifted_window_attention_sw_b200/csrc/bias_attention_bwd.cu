@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
       float v = flat_sum;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) bins[flat_bucket] += v;
+      if (lane == 0 && flat_bucket != kNoBucket) bins[flat_bucket] += v;
       __syncwarp();
       flat_sum = 0.f;
     };
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               if (at >= 8 * x && at - 8 * x < 39) v[k] += diag[x * 40 + at - 8 * x];
-            bucket[k] = at < 63 ? bl.bucket[at + 96 + c_first - 32 * (warp & 3)] : -1;
+            bucket[k] = at < 63 ? bl.bucket[at + 96 + c_first - 32 * (warp & 3)] : kNoBucket;
             const int before = __shfl_up_sync(0xffffffffu, bucket[k], 1);
             heads[k] = __ballot_sync(0xffffffffu, lane == 0 || before != bucket[k]);
             start[k] = 31 - __clz(heads[k] & (0xffffffffu >> (31 - lane)));
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const bool tail = bucket[k] >= 0 && (lane == 31 || ((heads[k] >> (lane + 1)) & 1));
+            const bool tail = bucket[k] != kNoBucket && (lane == 31 || ((heads[k] >> (lane + 1)) & 1));
             // runs that share a bucket (no map of vswin_bucket_map has them) add up into the first
             const uint32_t equal = __match_any_sync(0xffffffffu, tail ? bucket[k] : -2 - lane);
             const bool first = (equal & ((1u << lane) - 1)) == 0;

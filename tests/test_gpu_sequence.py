@@ -784,3 +784,27 @@ def test_adamw_8_gradient_whose_square_overflows():
         moved = (p[0] - before).abs()
         assert torch.isfinite(p[0][:512]).all()
         assert ((moved[512:] == 0) | moved[512:].isnan()).all()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_attention_gradient_leaves_bad_buckets_out(d, causal):
+    # offsets whose map entry lies outside the table have bias 0 and belong to no row of its gradient: the same as
+    # a further row of zeros in the table that they point to. Inside the map, and at its ends (tiles of one bucket)
+    L, buckets, D = 700, 8, 40
+    ins, do = _attn_inputs(BF16, 1, L, L, 2, 1, d, buckets=buckets)
+    ins[3][0] = 0  # (a tile of bucket 0 and a tile of no bucket have the same values)
+    good = vswin.bucket_map(buckets, D, True)
+    for ends in (False, True):
+        off = torch.zeros(2 * D + 1, dtype=torch.bool, device="cuda")
+        off[5:70:7] = True
+        off[0] = off[-1] = ends
+        bad = torch.where(off, torch.where(torch.arange(2 * D + 1, device="cuda") % 2 == 0, -1, 1 << 20).int(), good)
+        more = torch.cat((ins[3], torch.zeros_like(ins[3][:1])))
+        moved = torch.where(off, buckets, good.long()).int()
+        want = _attn_check([*ins[:3], more], moved, do, causal=causal)
+        out, lse = vswin.bias_attention_forward(*ins, bad, causal=causal)
+        got = out, lse, *vswin.bias_attention_backward(*ins, bad, out, lse, do, causal=causal)
+        assert vswin.poll_error() == vswin.ERR_BOUNDS
+        assert all(torch.equal(a, b) for a, b in zip(got[:5], want[:5]))
+        assert torch.equal(got[5], want[5][:buckets])
