@@ -85,7 +85,6 @@ template <class T, int D>
 __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const __grid_constant__ FwdParams params, Split sp) {
   const BiasAttnArgs& a = params.a;
   using C = FwdCfg<D>;
-  if (sp.n > 1) let_next_start();
   using Line = typename C::Line;
   constexpr int ST = C::ST, G = C::G, NBUF = C::NBUF, kBn = C::BN, kMmaWarp = C::kMmaWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -136,6 +135,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  if (sp.n > 1) let_next_start();
 
   if (warp > kMmaWarp) {
     // ------------------------------------------------------------ producers: tiles, bias lines

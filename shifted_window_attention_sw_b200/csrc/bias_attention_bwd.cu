@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
   using Line = typename C::Line;
   constexpr int G = C::G, ST = C::ST;
   constexpr int kMmaWarp = C::kWarps;
-  let_next_start();
   extern __shared__ __align__(1024) uint8_t smem[];
   const BiasAttnArgs& a = args.a;
   Line* lines = reinterpret_cast<Line*>(smem + C::OFF_LINE);
@@ -146,6 +145,8 @@ __global__ void __launch_bounds__(BwdCfg<D, kKeys>::THREADS, BwdCfg<D, kKeys>::C
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  // (not before this block has its columns: blocks of the pass that follows hold theirs while they wait for this one)
+  let_next_start();
   const uint32_t sf = smem_u32(smem + C::OFF_F), sm = smem_u32(smem + C::OFF_M);
   // the other pass, whose D this one reads (before any bounded wait; and the table's sums count on both having ended)
   if (kKeys) after_previous();

@@ -3,6 +3,8 @@ map, and the float64 definitions against central differences. CPU only."""
 
 import ctypes
 import math
+import os
+import re
 from fractions import Fraction
 
 import pytest
@@ -244,3 +246,21 @@ def test_ctypes_records_match_the_header():
     assert ctypes.sizeof(vswin._Heads) == 32 and ctypes.sizeof(vswin._Rotation) == 40
     assert ctypes.sizeof(vswin._BucketBias) == 24 and ctypes.sizeof(vswin._Visibility) == 32
     assert ctypes.sizeof(vswin._AdamwTensor) == 80
+
+
+def test_kernels_hold_their_tensor_memory_before_the_next_may_start():
+    """A kernel that lets its follower start early takes its tensor memory first. The follower's blocks hold theirs
+    while they wait for the whole kernel: one that had started, but not taken its own, could wait for them in turn."""
+    csrc = os.path.join(os.path.dirname(vswin.__file__), "csrc")
+    seen = 0
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for kernel in re.split(r"__global__", text)[1:]:
+            if "let_next_start()" not in kernel or "tmem_alloc(" not in kernel:
+                continue
+            seen += 1
+            # taken by one warp, so that the block has to meet before it speaks for all of its threads
+            taken = kernel.index("__syncthreads()", kernel.index("tmem_alloc("))
+            assert taken < kernel.index("let_next_start()"), name
+    assert seen >= 2
