@@ -98,6 +98,7 @@ class _AdamwTensor(ctypes.Structure):
                 ("n", _LL), ("weight_decay", ctypes.c_double), ("param_dtype", _I), ("grad_dtype", _I)]
 
 
+_data_ptr, _get_device, _is_contiguous = torch.Tensor.data_ptr, torch.Tensor.get_device, torch.Tensor.is_contiguous
 _RECORD_WORDS, _GRAD_WORD = ctypes.sizeof(_AdamwTensor) // 8, _AdamwTensor.grad.offset // 8
 
 
@@ -613,8 +614,10 @@ def bias_attention_backward(q, k, v, table, bucket_map, out, lse, dout, scale=No
 # ------------------------------------------------------------------ optimizer
 class AdamW:
     """AdamW over a list of contiguous weights on one CUDA device (see vswin_adamw_step): every step is one
-    launch per 192 tensors. The object owns the moments (zeros, or the ones given) and keeps the weights' list;
-    a weight may get another storage (``p.data = ...``), a moment or master is loaded by copying into it.
+    launch per 192 tensors. The object owns the moments (zeros, or the ones given) and keeps the weights' list.
+    A weight may get another storage (``p.data = ...``), and a moment, scale or master is loaded by copying into it
+    or by putting another tensor of its shape and type in its list (``m``, ``v``, ``m_scale``, ``v_scale``, ``master``);
+    a captured step keeps the storages that it was captured with.
 
     weight_decay: one value or one per weight. bits: 32 (float32 moments) or 8 (codes with a scale per 256
     elements). master: float32 copies that are stepped and rounded into the weights: True makes them, or a list.
@@ -660,25 +663,45 @@ class AdamW:
         self._records = (_AdamwTensor * len(self.params)).from_buffer(words)
         self._words = memoryview(words).cast("q")
         for i, (p, r) in enumerate(zip(self.params, self._records)):
-            dt, shape, n = DTYPES.get(p.dtype), p.shape, p.numel()
+            dt = DTYPES.get(p.dtype)
             if dt is None:
                 raise TypeError(f"params[{i}] must be one of {list(DTYPES)}, got {p.dtype}")
-            r.param = _flat(("params", i), p, shape, p.dtype, dev)
-            r.m = _flat(("m", i), self.m[i], shape, mt, dev)
-            r.v = _flat(("v", i), self.v[i], shape, vt, dev)
-            if bits == 8:
-                blocks_of = (-(-n // ADAMW_BLOCK),)
-                r.m_scale = _flat(("m_scale", i), self.m_scale[i], blocks_of, torch.float32, dev)
-                r.v_scale = _flat(("v_scale", i), self.v_scale[i], blocks_of, torch.float32, dev)
-            if self.master:
-                r.master = _flat(("master", i), self.master[i], shape, torch.float32, dev)
-            r.n, r.weight_decay, r.param_dtype = n, decay[i], dt
-        if len({r.param for r in self._records if r.n}) < sum(1 for r in self._records if r.n):
-            raise ValueError("a weight stands in params twice")
+            r.n, r.weight_decay, r.param_dtype = p.numel(), decay[i], dt
         self._shapes = [p.shape for p in self.params]
         self._indices = [dev.index] * len(self.params)
-        self._param_at = [p.data_ptr() for p in self.params]
         self._grad_types = None
+        self._record()
+
+    def _lists(self):
+        return self.params, self.m, self.v, self.m_scale, self.v_scale, self.master
+
+    def _addresses(self):
+        every = [*self.params, *self.m, *self.v]
+        if self.m_scale:
+            every += [*self.m_scale, *self.v_scale]
+        if self.master:
+            every += self.master
+        return list(map(_data_ptr, every))
+
+    def _record(self):
+        """Fills the records from the lists of weights and states as they are now."""
+        dev, states = self.device, (torch.float32, torch.float32) if self.bits == 32 else (torch.int8, torch.uint8)
+        self._recorded = None  # (until every record is right)
+        names = ("params", "m", "v", "m_scale", "v_scale", "master")
+        lists = [None if t is None else self._list(name, t) for name, t in zip(names, self._lists())]
+        for i, (r, shape) in enumerate(zip(self._records, self._shapes)):
+            at = [None if t is None else t[i] for t in lists]
+            scales = (-(-r.n // ADAMW_BLOCK),)
+            r.param = _flat(("params", i), at[0], shape, DTYPE_OF[r.param_dtype], dev)
+            r.m = _flat(("m", i), at[1], shape, states[0], dev)
+            r.v = _flat(("v", i), at[2], shape, states[1], dev)
+            r.m_scale = _flat(("m_scale", i), at[3], scales, torch.float32, dev)
+            r.v_scale = _flat(("v_scale", i), at[4], scales, torch.float32, dev)
+            r.master = _flat(("master", i), at[5], shape, torch.float32, dev)
+        if len({r.param for r in self._records if r.n}) < sum(1 for r in self._records if r.n):
+            raise ValueError("a weight stands in params twice")
+        # (held, so that another tensor in a list has another address)
+        self._held, self._recorded = lists, self._addresses()
 
     def _list(self, name, tensors):
         tensors = list(tensors)
@@ -693,8 +716,9 @@ class AdamW:
         grads = self._list("grads", grads)
         dev = self.device
         types = [g.dtype for g in grads]
-        if ([g.shape for g in grads] != self._shapes or [g.get_device() for g in grads] != self._indices
-                or not all([g.is_contiguous() for g in grads]) or not DTYPES.keys() >= set(types)):
+        if ([g.shape for g in grads] != self._shapes or list(map(_get_device, grads)) != self._indices
+                or not all(map(_is_contiguous, grads))
+                or types != self._grad_types and not DTYPES.keys() >= set(types)):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):
                 if g.dtype not in DTYPES or g.shape != shape or g.device != dev or not g.is_contiguous():
                     raise ValueError(f"grads[{i}] must be a contiguous {tuple(shape)} tensor of {list(DTYPES)} on "
@@ -703,24 +727,23 @@ class AdamW:
             for r, dtype in zip(self._records, types):
                 r.grad_dtype = DTYPES[dtype]
             self._grad_types = types
-        self._words[_GRAD_WORD::_RECORD_WORDS] = array.array("q", [g.data_ptr() for g in grads])
-        param_at = [p.data_ptr() for p in self.params]
-        if param_at != self._param_at:  # some weight's storage was exchanged
-            for i, (p, r, shape) in enumerate(zip(self.params, self._records, self._shapes)):
-                r.param = _flat(("params", i), p, shape, DTYPE_OF[r.param_dtype], dev)
-            self._param_at = param_at
+        self._words[_GRAD_WORD::_RECORD_WORDS] = array.array("q", list(map(_data_ptr, grads)))
+        if self._addresses() != self._recorded:  # some weight's or state's storage was exchanged
+            self._record()
         count, count_dev = self.steps + 1, None
-        if isinstance(step, torch.Tensor):
+        if step is None:
+            pass
+        elif type(step) is not int and isinstance(step, torch.Tensor):  # (the check of a tensor's class is a slow one)
             count_dev = _flat("step", step, tuple(step.shape), torch.int32, dev)
             if step.numel() != 1:
                 raise ValueError("step must have one element")
-        elif step is not None:
+        else:
             count = int(step)
         if grad_scale is not None and grad_scale.numel() != 1:
             raise ValueError("grad_scale must have one element")
         gs = None if grad_scale is None else _flat("grad_scale", grad_scale, tuple(grad_scale.shape), torch.float32, dev)
         _run(lib().vswin_adamw_step, dev, stream, self._records, len(self._records), self.bits,
-             float(self.lr if lr is None else lr), *map(float, self.betas), float(self.eps), count, count_dev, gs)
+             self.lr if lr is None else lr, *self.betas, self.eps, count, count_dev, gs)
         self.steps = count
         return self
 

@@ -808,3 +808,24 @@ def test_attention_gradient_leaves_bad_buckets_out(d, causal):
         assert vswin.poll_error() == vswin.ERR_BOUNDS
         assert all(torch.equal(a, b) for a, b in zip(got[:5], want[:5]))
         assert torch.equal(got[5], want[5][:buckets])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_follows_exchanged_states(bits):
+    # a moment, scale or copy put in its list is the one that steps, and the one that it replaces is left alone
+    p, g = _adamw_lists([700, 40], [BF16] * 2, [F32] * 2)
+    q = [t.clone() for t in p]
+    a, b = vswin.AdamW(p, bits=bits, master=True, **HYPER), vswin.AdamW(q, bits=bits, master=True, **HYPER)
+    names = ["m", "v", "master"] + (["m_scale", "v_scale"] if bits == 8 else [])
+    for _ in range(2):
+        old = {n: [t for t in getattr(a, n)] for n in names}
+        before = {n: [t.clone() for t in old[n]] for n in names}
+        for n in names:
+            for i, t in enumerate(old[n]):
+                getattr(a, n)[i] = t.clone()
+        a.step(g)
+        b.step(g)
+        for n in names:
+            assert all(torch.equal(x, y) for x, y in zip(getattr(a, n), getattr(b, n))), n
+            assert all(torch.equal(x, y) for x, y in zip(old[n], before[n])), n
+        assert all(torch.equal(x, y) for x, y in zip(p, q))

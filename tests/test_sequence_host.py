@@ -264,3 +264,39 @@ def test_kernels_hold_their_tensor_memory_before_the_next_may_start():
             taken = kernel.index("__syncthreads()", kernel.index("tmem_alloc("))
             assert taken < kernel.index("let_next_start()"), name
     assert seen >= 2
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_steps_the_tensors_that_stand_in_its_lists(monkeypatch, bits):
+    # the records of a step on tensors that are taken for CUDA ones; the library is not called
+    steps = []
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
+    monkeypatch.setattr(vswin, "lib", lambda: type("", (), {"vswin_adamw_step": None}))
+    monkeypatch.setattr(vswin, "_run", lambda fn, dev, stream, records, *a: steps.append(
+        [{n: getattr(r, "param" if n == "params" else n) for n in names} for r in records]))
+    names = ["params", "m", "v", "master"] + (["m_scale", "v_scale"] if bits == 8 else [])
+    opt = vswin.AdamW([torch.zeros(300), torch.zeros(7, 5)], bits=bits, master=True)
+    grads = [torch.ones(300), torch.ones(7, 5)]
+    at = lambda: [{n: getattr(opt, n)[i].data_ptr() for n in names} for i in range(2)]  # noqa: E731
+    opt.step(grads)
+    assert steps[-1] == at()
+    for n in names:
+        old = getattr(opt, n)[1]
+        getattr(opt, n)[1] = old.clone()
+        opt.step(grads)
+        assert steps[-1] == at() and steps[-1][1][n] != old.data_ptr(), n
+        getattr(opt, n)[0].data = getattr(opt, n)[0].clone()
+        opt.step(grads)
+        assert steps[-1] == at(), n
+        # one that does not fit is refused, and what was there is stepped on when it is put back
+        count, first, good = len(steps), opt.params[0], getattr(opt, n)[1]
+        opt.params[0], getattr(opt, n)[1] = first.clone(), torch.zeros(3, 3, dtype=old.dtype)
+        with pytest.raises(ValueError, match=rf"{n}\[1\]"):
+            opt.step(grads)
+        opt.params[0], getattr(opt, n)[1] = first, good
+        assert len(steps) == count
+        opt.step(grads)
+        assert steps[-1] == at(), n
+    opt.master = None
+    opt.step(grads)
+    assert [r["master"] for r in steps[-1]] == [None, None]
