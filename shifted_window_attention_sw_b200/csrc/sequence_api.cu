@@ -38,7 +38,7 @@ int check_view(const vswin_heads* v, const char* name, const Extent& e, size_t a
   const long long s[3] = {v->batch_stride, v->token_stride, v->head_stride};
   const long long n[3] = {e.B, e.L, e.H};
   for (int k = 0; k < 3; ++k) {
-    if (s[k] < 0 || s[k] > (1LL << 48) / n[k])
+    if (n[k] > 1 && (s[k] < 0 || s[k] > (1LL << 48) / n[k]))
       return fail(VSWIN_ERR_INVALID_ARG, "%s: stride %lld is negative or too large", name, s[k]);
     if (align > (size_t)esize && n[k] > 1 && (s[k] * esize) % (long long)align)
       return fail(VSWIN_ERR_INVALID_ARG, "%s: strides must be multiples of %zu bytes", name, align);

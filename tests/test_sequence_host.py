@@ -300,3 +300,27 @@ def test_adamw_steps_the_tensors_that_stand_in_its_lists(monkeypatch, bits):
     opt.master = None
     opt.step(grads)
     assert [r["master"] for r in steps[-1]] == [None, None]
+
+
+@pytest.mark.parametrize("stride", [-1, -2**63, 2**63 - 1, 3])
+def test_strides_of_extents_of_one_are_not_looked_at(L, stride):
+    # one sequence, one token or one head: such a stride is never used. What is refused is something else
+    before = vswin.launch_count()
+    lone = dict(batch_stride=stride, token_stride=stride, head_stride=stride)
+    one = [_view(n, 1, 1, 64, **lone) for n in range(1, 9)]
+    _refused(L, _norm(L, B=1, Lt=1, hq=1, hk=1, q=one[0], k=one[1], qo=one[4], ko=one[5], rot=_rot(dim=33)), before=before)
+    assert "rotation" in vswin.last_error()
+    _refused(L, _norm(L, B=1, Lt=1, hq=1, hk=1, q=one[0], k=one[1], qo=one[4], ko=one[5],
+                      back=dict(dq=one[6], dk=one[7], h=None)), before=before)
+    assert "dgamma" in vswin.last_error()
+    _refused(L, _attn(L, B=1, Lq=1, Lk=1, hq=1, hk=1, q=one[0], k=one[1], v=one[2], out=one[5], lse=0), before=before)
+    assert "lse" in vswin.last_error()
+    _refused(L, _attn(L, B=1, Lq=1, Lk=1, hq=1, hk=1, q=one[0], k=one[1], v=one[2], out=one[5],
+                      back=dict(do=one[7], dq=_view(9, 1, 1, 64, **lone), dk=_view(10, 1, 1, 64, **lone),
+                                dv=_view(11, 1, 1, 64, **lone), dt=None)), before=before)
+    assert "dtable" in vswin.last_error()
+    # with two of them it counts
+    lone["head_stride"] = 64
+    if stride != 3:
+        _refused(L, _norm(L, B=2, Lt=1, hq=1, hk=1, q=_view(1, 1, 1, 64, **lone), rot=_rot(dim=33)), before=before)
+        assert "stride" in vswin.last_error()
