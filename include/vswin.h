@@ -333,10 +333,10 @@ typedef struct {
  *   n = x / sqrt(mean_c(x^2) + eps) * gamma over the d channels of a head,
  *   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin) on the rotated pairs.
  * gamma_q, gamma_k [d] of the tensors' type (any dtype). d up to 256; rotation
- * may be NULL. q_out may be q itself and k_out k itself (the same view), else
- * they overlap neither. Arithmetic in fp32, one rounding. 16-byte loads when d
- * and dim are multiples of 16 and every row starts on 16 bytes, element by
- * element otherwise. No scratch.
+ * may be NULL. q_out may be q itself and k_out k itself (the same view); else an
+ * output shares no element with an input (slices of one buffer may interleave).
+ * Arithmetic in fp32, one rounding. 16-byte loads when d and dim are multiples of
+ * 16 and every row starts on 16 bytes, element by element otherwise. No scratch.
  */
 int vswin_qk_norm_forward(int dtype, int B, int L, int hq, int hk, int d, const vswin_heads* q, const vswin_heads* k,
                           const void* gamma_q, const void* gamma_k, float eps, const vswin_rotation* rotation,

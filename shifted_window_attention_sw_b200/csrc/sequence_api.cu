@@ -25,8 +25,51 @@ bool same_view(const Heads& a, const Heads& b) {
   return a.p == b.p && a.sb == b.sb && a.st == b.st && a.sh == b.sh;
 }
 
+// Whether `from`, moved by some steps (step k at most lo..hi times), comes into
+// (-below, above): the largest steps first, which leave few counts to try when the
+// smaller ones span less than they do (every view that holds no element twice).
+struct Steps {
+  int n = 0;
+  long long step[6], lo[6], hi[6];
+  void add(long long s, long long first, long long last) {
+    if (s == 0) return;
+    int at = 0;
+    while (at < n && step[at] > s) ++at;
+    if (at < n && step[at] == s) {
+      lo[at] += first, hi[at] += last;
+      return;
+    }
+    for (int k = n++; k > at; --k) step[k] = step[k - 1], lo[k] = lo[k - 1], hi[k] = hi[k - 1];
+    step[at] = s, lo[at] = first, hi[at] = last;
+  }
+  // (`tries` bounds the search; where it ends, the answer is yes)
+  bool reach(int k, long long from, long long below, long long above, int* tries) const {
+    if (k == n) return from > -below && from < above;
+    long long least = 0, most = 0;  // what the smaller steps can add
+    for (int j = k + 1; j < n; ++j) least += step[j] * lo[j], most += step[j] * hi[j];
+    auto floor_div = [](long long x, long long y) { return x / y - (x % y < 0); };
+    long long x = floor_div(-below - from - most, step[k]) + 1;
+    long long last = -floor_div(from + least - above, step[k]) - 1;
+    if (x < lo[k]) x = lo[k];
+    if (last > hi[k]) last = hi[k];
+    for (; x <= last; ++x)
+      if (--*tries < 0 || reach(k + 1, from + x * step[k], below, above, tries)) return true;
+    return false;
+  }
+};
+
+// Whether two views share an element: slices of one buffer may interleave without.
 bool views_overlap(const Heads& a, const Extent& ea, const Heads& b, const Extent& eb, int esize) {
-  return overlap(a.p, view_bytes(a, ea, esize), b.p, view_bytes(b, eb, esize));
+  if (!overlap(a.p, view_bytes(a, ea, esize), b.p, view_bytes(b, eb, esize))) return false;
+  Steps steps;
+  const long long sa[3] = {a.sb, a.st, a.sh}, na[3] = {ea.B, ea.L, ea.H};
+  const long long sb[3] = {b.sb, b.st, b.sh}, nb[3] = {eb.B, eb.L, eb.H};
+  for (int k = 0; k < 3; ++k) {
+    steps.add(sa[k] * esize, 0, na[k] - 1);
+    steps.add(sb[k] * esize, 1 - nb[k], 0);
+  }
+  int tries = 4096;
+  return steps.reach(0, static_cast<const char*>(a.p) - static_cast<const char*>(b.p), ea.d * esize, eb.d * esize, &tries);
 }
 
 // A view's pointer, alignment and strides; an output may not hold an element twice.
@@ -100,15 +143,12 @@ int check_qk_norm(int dtype, int B, int L, int hq, int hk, int d, const vswin_he
   for (int w = 0; w < 2; ++w) {
     const Heads& o = backward ? a->dx[w] : a->y[w];
     const char* on = backward ? gn[w] : yn[w];
-    const Heads* in[2] = {&a->x[w], backward ? &a->y[w] : nullptr};
-    bool replaces = false;
-    for (const Heads* i : in) replaces = replaces || (i && same_view(o, *i));
-    // (slices of one buffer interleave; the other tensor's view must not be this one)
-    if (replaces && (o.p == a->x[1 - w].p || (backward && o.p == a->y[1 - w].p)))
-      return fail(VSWIN_ERR_INVALID_ARG, "%s replaces a view that both q and k read", on);
-    for (int u = 0; u < 2 && !replaces; ++u)
-      if (views_overlap(o, ext[w], a->x[u], ext[u], es) || (backward && views_overlap(o, ext[w], a->y[u], ext[u], es)))
-        return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps an input without being the same view", on);
+    for (int u = 0; u < 2; ++u) {
+      const Heads* in[2] = {&a->x[u], backward ? &a->y[u] : nullptr};
+      for (const Heads* i : in)
+        if (i && !(u == w && same_view(o, *i)) && views_overlap(o, ext[w], *i, ext[u], es))
+          return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps an input that it does not replace", on);
+    }
   }
   if ((backward ? a->dx : a->y)[0].p == (backward ? a->dx : a->y)[1].p)
     return fail(VSWIN_ERR_INVALID_ARG, "%s and %s start at the same address", backward ? "dq" : "q_out",

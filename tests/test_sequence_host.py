@@ -4,6 +4,7 @@ map, and the float64 definitions against central differences. CPU only."""
 import ctypes
 import math
 import os
+import random
 import re
 from fractions import Fraction
 
@@ -324,3 +325,87 @@ def test_strides_of_extents_of_one_are_not_looked_at(L, stride):
     if stride != 3:
         _refused(L, _norm(L, B=2, Lt=1, hq=1, hk=1, q=_view(1, 1, 1, 64, **lone), rot=_rot(dim=33)), before=before)
         assert "stride" in vswin.last_error()
+
+
+# ------------------------------------------------------------------ what may share memory
+@pytest.fixture
+def no_launch(L):
+    # a call that passes its checks ends at the injected failure, before it touches a device
+    yield lambda: L.vswin_test_inject_failure(vswin.INJECT_CUDA, 1)
+    L.vswin_test_inject_failure(vswin.INJECT_CUDA, 0)
+
+
+def _verdict(L, no_launch, call):
+    """True when the call's arguments are accepted, False when they are refused."""
+    no_launch()
+    rc = call()
+    L.vswin_test_inject_failure(vswin.INJECT_CUDA, 0)
+    assert rc in (vswin.ERR_CUDA, vswin.ERR_INVALID_ARG), vswin.last_error()
+    assert rc == vswin.ERR_INVALID_ARG or "injected" in vswin.last_error()
+    return rc == vswin.ERR_CUDA
+
+
+def _slice(n, first, heads=8, Lt=8, d=64, es=2, **kw):
+    """Heads from `first` on of a (B, Lt, heads, d) buffer."""
+    return _view(n, Lt, heads, d, off=first * d * es, **kw)
+
+
+def test_norm_in_place_beside_the_other_tensor(L, no_launch):
+    ok = lambda **kw: _verdict(L, no_launch, lambda: _norm(L, **kw))  # noqa: E731
+    q, k = _slice(1, 0), _slice(1, 4)  # heads 0 to 3 and 4 to 5 of one buffer
+    assert ok(q=q, k=k, qo=q, ko=k) and ok(q=q, k=k, qo=q) and ok(q=q, k=k, ko=k)
+    for first in (1, 2, 3):  # k shares heads with the q that is replaced, or the other way round
+        k = _slice(1, first)
+        assert not ok(q=q, k=k, qo=q) and not ok(q=q, k=k, ko=k) and not ok(q=q, k=k, qo=q, ko=k)
+        assert ok(q=q, k=k)  # reading the same heads twice is fine
+    grads = lambda **kw: ok(back=dict(g=P(9), h=P(10), **kw))  # noqa: E731
+    a, b = _slice(7, 0), _slice(7, 4)
+    assert grads(dq=a, dk=b)
+    dy = dict(qo=_slice(5, 0), ko=_slice(5, 2))  # output gradients that share heads 2 and 3
+    back = lambda **kw: ok(**dy, back=kw)  # noqa: E731
+    assert not back(dq=_slice(5, 0)) and not back(dk=_slice(5, 2)) and back(dq=a, dk=b)
+    dy = dict(qo=_slice(5, 0), ko=_slice(5, 4))
+    assert back(dq=_slice(5, 0), dk=_slice(5, 4)) and back(dq=_slice(5, 0)) and not back(dq=_slice(5, 1))
+
+
+def test_results_may_interleave_with_inputs(L, no_launch):
+    # q, k and v of a projection, and the results in further heads of the same buffer, in either order of heads and tokens
+    for order in (dict(heads=16), dict(heads=16, batch_stride=16 * 8 * 64, token_stride=64, head_stride=8 * 64)):
+        s = lambda first: _view(1, 8, 16, 64, off=2 * first * (order.get("head_stride", 64)),  # noqa: E731
+                                **{n: x for n, x in order.items() if n != "heads"})
+        assert _verdict(L, no_launch, lambda: _norm(L, q=s(0), k=s(4), qo=s(8), ko=s(12)))
+        assert not _verdict(L, no_launch, lambda: _norm(L, q=s(0), k=s(4), qo=s(3), ko=s(12)))
+        assert _verdict(L, no_launch, lambda: _attn(L, q=s(0), k=s(4), v=s(6), out=s(8)))
+        assert not _verdict(L, no_launch, lambda: _attn(L, q=s(0), k=s(4), v=s(6), out=s(5)))
+        assert _verdict(L, no_launch, lambda: _attn(L, q=s(0), k=s(4), v=s(6), out=s(8), back=dict(dv=s(12), dk=s(14))))
+        assert not _verdict(L, no_launch, lambda: _attn(L, q=s(0), k=s(4), v=s(6), out=s(8), back=dict(dv=s(11), dk=s(14))))
+
+
+def _elements(off, n, s, d):
+    return {off + b * s[0] + t * s[1] + h * s[2] + c for b in range(n[0]) for t in range(n[1]) for h in range(n[2])
+            for c in range(d)}
+
+
+def test_overlap_of_any_two_views(L, no_launch):
+    # an output and an input of random extents and strides: refused when an element is in both, and only then
+    rng = random.Random(5)
+    seen = {True: 0, False: 0}
+    for _ in range(3000):
+        d, n = rng.choice([1, 2, 3, 5]), [rng.randint(1, 3) for _ in range(3)]
+        dims = rng.sample(range(3), 3)
+        so, span = [0, 0, 0], d
+        for k in dims:  # an output holds nothing twice
+            so[k] = span + rng.choice([0, 0, 1, 4, 11])
+            span += (n[k] - 1) * so[k]
+        si = so if rng.random() < 0.3 else [rng.choice([0, 1, 2, d, 2 * d, 3 * d + 1, 17]) for _ in range(3)]
+        hk, off = rng.randint(1, 3), rng.randint(-40, 40)
+        view = lambda off, s: vswin._Heads(P(1) + 2 * off, *s)  # noqa: E731
+        q, qo = view(off, si), view(0, so)
+        if off == 0 and all(a == b or m == 1 for a, b, m in zip(si, so, n)):
+            continue  # in place
+        shared = bool(_elements(0, n, so, d) & _elements(off, n, si, d))
+        got = _verdict(L, no_launch, lambda: _norm(L, B=n[0], Lt=n[1], hq=n[2], hk=hk, d=d, q=q, qo=qo,
+                                                   k=_view(2, n[1], hk, d), ko=_view(3, n[1], hk, d)))
+        assert got == (not shared), (d, n, so, si, off)
+        seen[shared] += 1
+    assert min(seen.values()) > 300, seen
