@@ -334,7 +334,8 @@ typedef struct {
  *   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin) on the rotated pairs.
  * gamma_q, gamma_k [d] of the tensors' type (any dtype). d up to 256; rotation
  * may be NULL. q_out may be q itself and k_out k itself (the same view); else an
- * output shares no element with an input (slices of one buffer may interleave).
+ * output shares no element with an input or the other output (slices of one
+ * buffer may interleave).
  * Arithmetic in fp32, one rounding. 16-byte loads when d and dim are multiples of
  * 16 and every row starts on 16 bytes, element by element otherwise. No scratch.
  */
@@ -416,9 +417,9 @@ int vswin_bias_attention_forward(int dtype, int B, int Lq, int Lk, int hq, int h
  * (B, Lq, hq, d), dk, dv (B, Lk, hk, d; summed over the heads that share them)
  * and dtable [buckets][hq], all of the tensors' type, summed in fp32 and rounded
  * once, overwritten. Zero for rows and keys that take no part. The gradients
- * overlap no input; dq, dk and dv may be slices of one buffer. Scratch: from the
- * library's pool, 4 bytes per query row and head and 4 bytes per bucket, head
- * and 128 query rows of a sequence.
+ * share no element with an input or one another (slices of one buffer may
+ * interleave). Scratch: from the library's pool, 4 bytes per query row and head
+ * and 4 bytes per bucket, head and 128 query rows of a sequence.
  */
 int vswin_bias_attention_backward(int dtype, int B, int Lq, int Lk, int hq, int hk, int d, const vswin_heads* q,
                                   const vswin_heads* k, const vswin_heads* v, float scale,

@@ -150,9 +150,9 @@ int check_qk_norm(int dtype, int B, int L, int hq, int hk, int d, const vswin_he
           return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps an input that it does not replace", on);
     }
   }
-  if ((backward ? a->dx : a->y)[0].p == (backward ? a->dx : a->y)[1].p)
-    return fail(VSWIN_ERR_INVALID_ARG, "%s and %s start at the same address", backward ? "dq" : "q_out",
-                backward ? "dk" : "k_out");
+  const Heads* out = backward ? a->dx : a->y;
+  if (views_overlap(out[0], ext[0], out[1], ext[1], es))
+    return fail(VSWIN_ERR_INVALID_ARG, "%s and %s overlap", backward ? "dq" : "q_out", backward ? "dk" : "k_out");
   if (r) {
     if (r->dim < 0 || r->dim > d || r->dim % 2)
       return fail(VSWIN_ERR_INVALID_ARG, "rotation dim %d must be even and within [0, %d]", r->dim, d);
@@ -360,8 +360,8 @@ int vswin_bias_attention_backward(int dtype, int B, int Lq, int Lk, int hq, int 
         return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps an input", names[o]);
     if (overlap(outs[o]->p, n, lse, lse_n) || overlap(outs[o]->p, n, a.table, tb) || overlap(outs[o]->p, n, dtable, tb))
       return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps lse, the table or its gradient", names[o]);
-    if (outs[o]->p == outs[(o + 1) % 3]->p)
-      return fail(VSWIN_ERR_INVALID_ARG, "%s and %s start at the same address", names[o], names[(o + 1) % 3]);
+    if (views_overlap(*outs[o], out_e[o], *outs[(o + 1) % 3], out_e[(o + 1) % 3], 2))
+      return fail(VSWIN_ERR_INVALID_ARG, "%s and %s overlap", names[o], names[(o + 1) % 3]);
   }
   for (int i = 0; i < 5; ++i)
     if (overlap(dtable, tb, ins[i]->p, view_bytes(*ins[i], in_e[i], 2)))

@@ -409,3 +409,18 @@ def test_overlap_of_any_two_views(L, no_launch):
         assert got == (not shared), (d, n, so, si, off)
         seen[shared] += 1
     assert min(seen.values()) > 300, seen
+
+
+def test_results_that_share_elements_are_refused(L, no_launch):
+    # results of one call in one buffer: neighbouring heads or interleaved channels are fine, shared ones are not
+    ok = lambda call: _verdict(L, no_launch, call)  # noqa: E731
+    for first, good in ((4, True), (3, False), (1, False), (0, False)):
+        assert ok(lambda: _norm(L, qo=_slice(5, 0), ko=_slice(5, first))) == good, first
+        assert ok(lambda: _norm(L, back=dict(dq=_slice(7, 0), dk=_slice(7, first)))) == good, first
+        assert ok(lambda: _attn(L, back=dict(dq=_slice(9, 0), dk=_slice(9, first)))) == good, first
+        assert ok(lambda: _attn(L, back=dict(dq=_slice(9, 0), dv=_slice(9, first)))) == good, first
+    for first, good in ((2, True), (1, False), (0, False)):
+        assert ok(lambda: _attn(L, back=dict(dk=_slice(9, 4), dv=_slice(9, 4 + first), dq=_slice(9, 0)))) == good, first
+    pair = lambda n, at: _view(n, 8, 4, 64, off=2 * at, batch_stride=8 * 4 * 128, token_stride=4 * 128, head_stride=128)  # noqa: E731
+    assert ok(lambda: _norm(L, hk=4, qo=pair(5, 0), ko=pair(5, 64)))
+    assert not ok(lambda: _norm(L, hk=4, qo=pair(5, 0), ko=pair(5, 63)))
