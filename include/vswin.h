@@ -309,7 +309,9 @@ typedef enum { VSWIN_BF16 = 0, VSWIN_FP16 = 1, VSWIN_F32 = 2 } vswin_dtype;
 /* A (batch, token, head, channel) tensor on the device: channels contiguous,
  * the other strides in elements (any order; q, k and v may be slices of one
  * projection's output). An output may not hold one element twice; an input may
- * (stride 0). Strides of dimensions of extent 1 are not looked at. */
+ * (stride 0). Strides of dimensions of extent 1 are not looked at. No result of
+ * an operator lies over weights, angles, positions, a bias table or its map,
+ * lengths or starts that the call reads. */
 typedef struct {
   void* data;
   long long batch_stride, token_stride, head_stride;

@@ -103,6 +103,34 @@ int check_view(const vswin_heads* v, const char* name, const Extent& e, size_t a
   return VSWIN_OK;
 }
 
+// Contiguous memory that a call reads beside its views (p may be NULL).
+struct Flat {
+  const void* p;
+  size_t bytes;
+};
+
+bool overlaps_any(const void* p, size_t bytes, const Flat* f, int n) {
+  for (int k = 0; k < n; ++k)
+    if (f[k].p && overlap(p, bytes, f[k].p, f[k].bytes)) return true;
+  return false;
+}
+
+// The weights, angles and positions of the norm, and what of the bias and the
+// visibility is on the device.
+constexpr int kNormFlats = 5, kAttnFlats = 5;
+void norm_flats(const QkNormArgs& a, int esize, Flat (&f)[kNormFlats]) {
+  const size_t gamma = (size_t)a.d * esize, angles = (size_t)a.rows * (a.rot / 2) * 4;
+  const bool turns = a.rot > 0;
+  f[0] = {a.gamma[0], gamma}, f[1] = {a.gamma[1], gamma};
+  f[2] = {turns ? a.cosp : nullptr, angles}, f[3] = {turns ? a.sinp : nullptr, angles};
+  f[4] = {turns ? a.positions : nullptr, (size_t)a.B * a.L * 4};
+}
+void attention_flats(const BiasAttnArgs& a, Flat (&f)[kAttnFlats]) {
+  const size_t per_sequence = (size_t)a.B * 4;
+  f[0] = {a.table, (size_t)a.buckets * a.hq * 2}, f[1] = {a.map, (2 * (size_t)a.D + 1) * 4};
+  f[2] = {a.q_lens, per_sequence}, f[3] = {a.kv_lens, per_sequence}, f[4] = {a.q_start, per_sequence};
+}
+
 // Sizes, views, weights and rotation of the norm; `backward` has output
 // gradients in y and input gradients in dx.
 int check_qk_norm(int dtype, int B, int L, int hq, int hk, int d, const vswin_heads* q, const vswin_heads* k,
@@ -170,6 +198,11 @@ int check_qk_norm(int dtype, int B, int L, int hq, int hk, int d, const vswin_he
     a->positions = r->positions;
     a->rows = r->rows;
   }
+  Flat flats[kNormFlats];
+  norm_flats(*a, es, flats);
+  for (int w = 0; w < 2; ++w)
+    if (overlaps_any(out[w].p, view_bytes(out[w], ext[w], es), flats, kNormFlats))
+      return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps a gamma, a rotation table or the positions", backward ? gn[w] : yn[w]);
   return VSWIN_OK;
 }
 
@@ -253,13 +286,15 @@ int vswin_qk_norm_backward(int dtype, int B, int L, int hq, int hk, int d, const
   int st = check_qk_norm(dtype, B, L, hq, hk, d, q, k, gamma_q, gamma_k, eps, rotation, dq_out, dk_out, dq, dk, &a);
   if (st != VSWIN_OK) return st;
   float* dg[2] = {dgamma_q, dgamma_k};
+  Flat flats[kNormFlats];
+  norm_flats(a, elem_bytes(dtype), flats);
   for (int w = 0; w < 2; ++w) {
     if (!dg[w] || !aligned(dg[w], 4)) return fail(VSWIN_ERR_INVALID_ARG, "dgamma is NULL or not 4-byte aligned");
     const size_t n = (size_t)d * 4, es = elem_bytes(dtype);
     for (int u = 0; u < 2; ++u) {
       const Extent e{B, L, u ? hk : hq, d};
       if (overlap(dg[w], n, a.x[u].p, view_bytes(a.x[u], e, es)) || overlap(dg[w], n, a.y[u].p, view_bytes(a.y[u], e, es)) ||
-          overlap(dg[w], n, a.dx[u].p, view_bytes(a.dx[u], e, es)) || overlap(dg[w], n, a.gamma[u], d * es))
+          overlap(dg[w], n, a.dx[u].p, view_bytes(a.dx[u], e, es)) || overlaps_any(dg[w], n, flats, kNormFlats))
         return fail(VSWIN_ERR_INVALID_ARG, "dgamma overlaps another tensor");
     }
     a.dgamma[w] = dg[w];
@@ -315,6 +350,10 @@ int vswin_bias_attention_forward(int dtype, int B, int Lq, int Lk, int hq, int h
   if (overlap(lse, lse_n, a.o.p, view_bytes(a.o, eq, 2)) || overlap(lse, lse_n, a.q.p, view_bytes(a.q, eq, 2)) ||
       overlap(lse, lse_n, a.k.p, view_bytes(a.k, ek, 2)) || overlap(lse, lse_n, a.v.p, view_bytes(a.v, ek, 2)))
     return fail(VSWIN_ERR_INVALID_ARG, "lse overlaps another tensor");
+  Flat flats[kAttnFlats];
+  attention_flats(a, flats);
+  if (overlaps_any(a.o.p, view_bytes(a.o, eq, 2), flats, kAttnFlats) || overlaps_any(lse, lse_n, flats, kAttnFlats))
+    return fail(VSWIN_ERR_INVALID_ARG, "out or lse overlaps the bias table, its map, lengths or starts");
   st = make_ctx(&a.ctx);
   if (st != VSWIN_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -353,21 +392,23 @@ int vswin_bias_attention_backward(int dtype, int B, int Lq, int Lk, int hq, int 
   const Heads* outs[] = {&a.dq, &a.dk, &a.dv};
   const Extent out_e[] = {eq, ek, ek};
   const char* names[] = {"dq", "dk", "dv"};
+  Flat flats[kAttnFlats];
+  attention_flats(a, flats);
   for (int o = 0; o < 3; ++o) {
     const size_t n = view_bytes(*outs[o], out_e[o], 2);
     for (int i = 0; i < 5; ++i)
       if (views_overlap(*outs[o], out_e[o], *ins[i], in_e[i], 2))
         return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps an input", names[o]);
-    if (overlap(outs[o]->p, n, lse, lse_n) || overlap(outs[o]->p, n, a.table, tb) || overlap(outs[o]->p, n, dtable, tb))
-      return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps lse, the table or its gradient", names[o]);
+    if (overlap(outs[o]->p, n, lse, lse_n) || overlap(outs[o]->p, n, dtable, tb) || overlaps_any(outs[o]->p, n, flats, kAttnFlats))
+      return fail(VSWIN_ERR_INVALID_ARG, "%s overlaps lse, the bias table, its gradient or map, lengths or starts", names[o]);
     if (views_overlap(*outs[o], out_e[o], *outs[(o + 1) % 3], out_e[(o + 1) % 3], 2))
       return fail(VSWIN_ERR_INVALID_ARG, "%s and %s overlap", names[o], names[(o + 1) % 3]);
   }
   for (int i = 0; i < 5; ++i)
     if (overlap(dtable, tb, ins[i]->p, view_bytes(*ins[i], in_e[i], 2)))
       return fail(VSWIN_ERR_INVALID_ARG, "dtable overlaps an input");
-  if (overlap(dtable, tb, lse, lse_n) || overlap(dtable, tb, a.table, tb))
-    return fail(VSWIN_ERR_INVALID_ARG, "dtable overlaps lse or the table");
+  if (overlap(dtable, tb, lse, lse_n) || overlaps_any(dtable, tb, flats, kAttnFlats))
+    return fail(VSWIN_ERR_INVALID_ARG, "dtable overlaps lse, the table, its map, lengths or starts");
   st = make_ctx(&a.ctx);
   if (st != VSWIN_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -405,7 +405,7 @@ def test_overlap_of_any_two_views(L, no_launch):
             continue  # in place
         shared = bool(_elements(0, n, so, d) & _elements(off, n, si, d))
         got = _verdict(L, no_launch, lambda: _norm(L, B=n[0], Lt=n[1], hq=n[2], hk=hk, d=d, q=q, qo=qo,
-                                                   k=_view(2, n[1], hk, d), ko=_view(3, n[1], hk, d)))
+                                                   k=_view(2, n[1], hk, d), ko=_view(6, n[1], hk, d)))
         assert got == (not shared), (d, n, so, si, off)
         seen[shared] += 1
     assert min(seen.values()) > 300, seen
@@ -424,3 +424,27 @@ def test_results_that_share_elements_are_refused(L, no_launch):
     pair = lambda n, at: _view(n, 8, 4, 64, off=2 * at, batch_stride=8 * 4 * 128, token_stride=4 * 128, head_stride=128)  # noqa: E731
     assert ok(lambda: _norm(L, hk=4, qo=pair(5, 0), ko=pair(5, 64)))
     assert not ok(lambda: _norm(L, hk=4, qo=pair(5, 0), ko=pair(5, 63)))
+
+
+def test_results_over_what_a_call_reads_beside_the_views(L, no_launch):
+    # weights, angles, positions, the bias table and its map, lengths and starts: no result lies over one of them
+    ok = lambda call: _verdict(L, no_launch, call)  # noqa: E731
+    rot = lambda **kw: _rot(**{**dict(dim=32, rows=8, positions=P(13)), **kw})  # noqa: E731
+    assert ok(lambda: _norm(L, rot=rot())) and ok(lambda: _norm(L, rot=rot(), back={}))
+    size = 2 * 8 * 4 * 64 * 2  # bytes of q_out
+    for at in (0, size - 64):  # at its first element, and over its last ones
+        for kw in (dict(gq=5), dict(gk=5), dict(rot=rot(cos=5)), dict(rot=rot(sin=5)), dict(rot=rot(positions=P(5)))):
+            qo = _view(5, 8, 4, 64, off=-at)
+            assert not ok(lambda: _norm(L, **{**dict(rot=rot(), qo=qo), **kw})), (at, kw)
+        for kw in (dict(gq=7), dict(gk=7), dict(rot=rot(cos=7)), dict(rot=rot(sin=7)), dict(rot=rot(positions=P(7)))):
+            assert not ok(lambda: _norm(L, **{**dict(rot=rot()), **kw}, back=dict(dq=_view(7, 8, 4, 64, off=-at)))), (at, kw)
+    for kw in (dict(rot=rot(cos=9)), dict(rot=rot(sin=10)), dict(rot=rot(positions=P(9)))):
+        assert not ok(lambda: _norm(L, **kw, back={})), kw
+    lens = lambda a=14, b=15, c=16: vswin._Visibility(P(a), P(b), P(c), 1)  # noqa: E731
+    assert ok(lambda: _attn(L, vis=lens())) and ok(lambda: _attn(L, vis=lens(), back={}))
+    for n in (6, 7):  # out, lse
+        for kw in (dict(table=n), dict(bmap=n), dict(vis=lens(a=n)), dict(vis=lens(b=n)), dict(vis=lens(c=n))):
+            assert not ok(lambda: _attn(L, **{**dict(vis=lens()), **kw})), (n, kw)
+    for n in (9, 10, 11, 12):  # dq, dk, dv, dtable
+        for kw in (dict(table=n), dict(bmap=n), dict(vis=lens(a=n)), dict(vis=lens(b=n)), dict(vis=lens(c=n))):
+            assert not ok(lambda: _attn(L, **{**dict(vis=lens()), **kw}, back={})), (n, kw)
