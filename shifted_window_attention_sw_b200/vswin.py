@@ -74,6 +74,8 @@ _LL = ctypes.c_longlong
 # vswin_dtype
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 DTYPE_OF = {number: dtype for dtype, number in DTYPES.items()}
+MAX_DISTANCE = 1 << 20  # of a bucket map
+_INT_MAX = 2**31 - 1
 ADAMW_BLOCK = 256  # elements that share one scale of the 8-bit moments
 
 
@@ -550,9 +552,10 @@ def qk_norm_backward(q, k, gamma_q, gamma_k, dq_out, dk_out, eps=1e-6, cos=None,
 def bucket_map(buckets, max_distance, bidirectional=True, device="cuda"):
     """int32 tensor [2 * max_distance + 1]: the bucket of each offset key - query in [-max_distance,
     max_distance] (see vswin_bucket_map), as the attention with bucketed bias takes it."""
-    out = torch.empty(2 * max(int(max_distance), 0) + 1, dtype=torch.int32)
-    _check(lib().vswin_bucket_map(int(buckets), int(max_distance), 1 if bidirectional else 0,
-                                  ctypes.cast(out.data_ptr(), _IP)))
+    # (the library refuses what lies outside; ctypes would pass the low 32 bits of more)
+    buckets, max_distance = min(max(int(buckets), 0), _INT_MAX), min(max(int(max_distance), 0), MAX_DISTANCE + 1)
+    out = torch.empty(2 * max_distance + 1, dtype=torch.int32)
+    _check(lib().vswin_bucket_map(buckets, max_distance, 1 if bidirectional else 0, ctypes.cast(out.data_ptr(), _IP)))
     return out.to(device)
 
 

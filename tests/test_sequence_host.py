@@ -448,3 +448,11 @@ def test_results_over_what_a_call_reads_beside_the_views(L, no_launch):
     for n in (9, 10, 11, 12):  # dq, dk, dv, dtable
         for kw in (dict(table=n), dict(bmap=n), dict(vis=lens(a=n)), dict(vis=lens(b=n)), dict(vis=lens(c=n))):
             assert not ok(lambda: _attn(L, **{**dict(vis=lens()), **kw}, back={})), (n, kw)
+
+
+@pytest.mark.parametrize("args", [(32, 2**32 + 128, True), (2**32 + 32, 128, True), (32, -2**40, False), (-2**33 + 32, 128, False),
+                                  (32, 10**15, True)])
+def test_bucket_map_refuses_what_an_int_does_not_hold(L, args):
+    with pytest.raises(vswin.VswinError) as e:
+        vswin.bucket_map(*args, device="cpu")
+    assert e.value.status == vswin.ERR_INVALID_ARG
