@@ -499,6 +499,8 @@ def _qk_norm_args(q, k, gamma_q, gamma_k, eps, cos, sin, positions, interleaved)
         raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(shape)} and {tuple(k_shape)}")
     B, L, hq, d = shape
     hk, dt, dev = k_shape[2], q.dtype, q.device
+    if max(*shape, hk) > _INT_MAX:  # (ctypes would pass the low 32 bits)
+        raise VswinError(ERR_UNSUPPORTED, f"sizes of q {tuple(shape)} or k {tuple(k_shape)} exceed 2^31 - 1")
     code = DTYPES.get(dt)
     if code is None:
         raise TypeError(f"q must be one of {list(DTYPES)}, got {dt}")
@@ -565,6 +567,8 @@ def _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens, kv_l
         raise ValueError(f"q and k must be (B, L, heads, d), got {tuple(shape)} and {tuple(k_shape)}")
     B, Lq, hq, d = shape
     Lk, hk, dt, dev = k_shape[1], k_shape[2], q.dtype, q.device
+    if max(*shape, Lk, hk) > _INT_MAX:  # (ctypes would pass the low 32 bits)
+        raise VswinError(ERR_UNSUPPORTED, f"sizes of q {tuple(shape)} or k {tuple(k_shape)} exceed 2^31 - 1")
     code = DTYPES.get(dt)
     if code is None:
         raise TypeError(f"q must be torch.bfloat16 or torch.float16, got {dt}")

@@ -456,3 +456,19 @@ def test_bucket_map_refuses_what_an_int_does_not_hold(L, args):
     with pytest.raises(vswin.VswinError) as e:
         vswin.bucket_map(*args, device="cpu")
     assert e.value.status == vswin.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dim", [0, 1, 2])
+def test_binding_refuses_extents_that_an_int_does_not_hold(dim):
+    # (broadcast views: nothing of that size is in memory)
+    wide = [1, 1, 1, 64]
+    wide[dim] = 2**32 + 1
+    one = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    x, w, t, m = one.expand(wide), one[0, 0, 0], torch.zeros(2, 1, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: vswin.qk_norm_forward(x, x, w, w), lambda: vswin.qk_norm_backward(x, x, w, w, x, x),
+                 lambda: vswin.bias_attention_forward(x, x, x, t, m),
+                 lambda: vswin.bias_attention_backward(x, x, x, t, m, x, None, x),
+                 *((lambda: vswin.bias_attention_forward(one, x, x, t, m),) if dim == 1 else ())):
+        with pytest.raises(vswin.VswinError) as e:
+            call()
+        assert e.value.status == vswin.ERR_UNSUPPORTED
