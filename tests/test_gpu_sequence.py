@@ -829,3 +829,58 @@ def test_adamw_follows_exchanged_states(bits):
             assert all(torch.equal(x, y) for x, y in zip(getattr(a, n), getattr(b, n))), n
             assert all(torch.equal(x, y) for x, y in zip(old[n], before[n])), n
         assert all(torch.equal(x, y) for x, y in zip(p, q))
+
+
+@pytest.mark.parametrize("master", [None, True])
+@pytest.mark.parametrize("ptype,gtype", [(BF16, BF16), (FP16, FP16), (F32, BF16), (BF16, F32)], ids=str)
+def test_adamw_8_in_every_form(ptype, gtype, master):
+    # copies, gradients' types and factor, and two launches' worth of tensors that start anywhere
+    sizes = [1 + (211 * i) % 700 for i in range(200)]
+    p, g = _adamw_lists(sizes, [ptype] * 200, [gtype] * 200, offset=1)
+    opt = vswin.AdamW(p, bits=8, weight_decay=0.1, master=master, **HYPER)
+    gs = torch.tensor([0.5], device="cuda")
+    for step in (1, 2):
+        want = [_adamw_8_definition(opt, p[i], g[i], i, 0.1, step, 0.5, opt.master[i] if master else None)
+                for i in range(200)]
+        opt.step(g, grad_scale=gs)
+        for i, (w, m, v) in enumerate(want):
+            n = sizes[i]
+            if master:
+                _close("master", opt.master[i], w, 2e-6 * (w.abs() + HYPER["lr"]))
+                assert torch.equal(p[i], opt.master[i].to(ptype))
+            else:
+                _adamw_bounds(w, p[i], ptype)
+            sm, sv = _block_max(m, n), _block_max(v, n)
+            _close("m_scale", opt.m_scale[i], sm, 1e-6 * sm)
+            _close("v_scale", opt.v_scale[i], sv, 1e-6 * sv)
+            at = torch.arange(n, device="cuda") // 256
+            # the nearest codes, up to fp32 errors of a few 2^-24 of the argument at a tie
+            assert ((opt.m[i].double().abs() - 127 * (m.abs() / sm[at]).sqrt()).abs() <= 0.5 + 1e-4).all()
+            assert (opt.m[i].double() * m >= 0).all()
+            assert ((opt.v[i].double() - (255 * (v / sv[at]) ** 0.25).clamp(min=1)).abs() <= 0.5 + 1e-4).all()
+
+
+@pytest.mark.parametrize("dtype,B,L,hq,hk,d,causal", [
+    (FP16, 1, 2113, 16, 4, 128, True), (BF16, 1, 1500, 32, 1, 64, True), (BF16, 2, 1217, 8, 2, 32, False),
+    (FP16, 1, 5003, 2, 1, 64, True), (BF16, 1, 5003, 2, 2, 128, False),
+], ids=str)
+def test_attention_gradient_of_long_sequences_and_shared_heads(dtype, B, L, hq, hk, d, causal):
+    ins, do = _attn_inputs(dtype, B, L, L, hq, hk, d)
+    lens = _i32(*[L - 37 * b for b in range(B)])
+    _attn_check(ins, _map(bidirectional=not causal), do, causal=causal, q_lens=lens, kv_lens=lens)
+
+
+def test_two_layers_at_once():
+    # the whole chain on two streams at the same time, many times over: the same bits as alone
+    i, do = _layer_inputs(2, 600)
+    kw = dict(causal=True)
+    want = _layer(i, kw, do, True)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(_layer(i, kw, do, True))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
