@@ -350,7 +350,8 @@ int vswin_qk_norm_forward(int dtype, int B, int L, int hq, int hk, int d, const 
  * the same view as the input or the output gradient they come from) and
  * dgamma_q, dgamma_k (float [d], overwritten). Deterministic: the rows' shares
  * of dgamma are added in a fixed order. Scratch: 4 d bytes per block of the
- * launch (at most a few hundred KB), from the library's pool.
+ * launch (at most 0.3 MB, or 1.2 MB where rows go element by element), from the
+ * library's pool.
  */
 int vswin_qk_norm_backward(int dtype, int B, int L, int hq, int hk, int d, const vswin_heads* q, const vswin_heads* k,
                            const void* gamma_q, const void* gamma_k, float eps, const vswin_rotation* rotation,
@@ -420,8 +421,14 @@ int vswin_bias_attention_forward(int dtype, int B, int Lq, int Lk, int hq, int h
  * and dtable [buckets][hq], all of the tensors' type, summed in fp32 and rounded
  * once, overwritten. Zero for rows and keys that take no part. The gradients
  * share no element with an input or one another (slices of one buffer may
- * interleave). Scratch: from the library's pool, 4 bytes per query row and head
- * and 4 bytes per bucket, head and 128 query rows of a sequence.
+ * interleave). P and the gradient dS of the scores are rounded to the tensors'
+ * type as operands, and fp16 has steps of 2^-24 below 6.1e-5 whatever the value:
+ * there dout has to be large enough (scaled by a power of two, the gradients
+ * scaled back) for P dout v to lie above that. 4096 keys and normal inputs of
+ * width 64: dq and dk off by 3e-4 of their norm for dout of 1, 5e-4 for 1e-2,
+ * 5e-2 for 1e-4 (bf16: 2.4e-3 for each). Scratch: from the library's pool, 4
+ * bytes per query row and head and 4 bytes per bucket, head and 128 query rows
+ * of a sequence.
  */
 int vswin_bias_attention_backward(int dtype, int B, int Lq, int Lk, int hq, int hk, int d, const vswin_heads* q,
                                   const vswin_heads* k, const vswin_heads* v, float scale,
@@ -441,12 +448,18 @@ int vswin_bias_attention_backward(int dtype, int B, int Lq, int Lk, int hq, int 
  * scale (float [ceil(n / 256)], the block's largest value):
  *   m = m_scale sgn(c) (c / 127)^2,  v = v_scale (c / 255)^4,
  * rounded to the nearest code in that spacing; a positive v never reads back as
- * zero. All-zero codes and scales are zero moments.
+ * zero. Both hold for blocks whose largest m or v is at least 2^-100 (8e-31); below
+ * that m reads back as zero, and every positive v has code 1. All-zero codes and
+ * scales are zero moments. A block with an infinite or NaN moment (a gradient whose
+ * square overflows is enough) has that scale: its moments read back as infinite or
+ * NaN, its weights stand still or become NaN. The denominator of an 8-bit step is
+ * at least 2^-66, which counts only with an eps below that.
  * The list is a host array and is not kept; its records travel with the launch
  * (one launch per 192 tensors), so that a step can be captured. A captured step
  * takes its count from step_device (one int on the device, from 1; `step` is
  * then not looked at) and, as any step may, the factor of the gradients from
- * grad_scale (one float on the device, or NULL). A tensor's buffers may not
+ * grad_scale (one float on the device, or NULL); lr, the betas, eps and the
+ * weight decays are those of the capture. A tensor's buffers may not
  * overlap one another; two tensors of a list may not share buffers (not checked).
  */
 typedef struct {

@@ -17,9 +17,10 @@
 // is done. D = 32 and 64: two groups of four warps take the tiles in turns, each
 // with its own softmax statistics and sums, joined at the end (sixteen softmax
 // warps per SM), half a tile in registers at a time. D = 128: TMEM has room for
-// one group's sums; it takes a whole tile at a time (8192 causal tokens, 16 heads
-// over 4: 263 us; half tiles 300; tiles of 128 keys with one score buffer 276;
-// eight warps that share a tile's columns 279). One warp brings K and V tiles
+// one group's sums (two CTAs of 256 columns); it takes a whole tile at a time (8192
+// causal tokens, 16 heads over 4, short runs: 263 us; half tiles 300; tiles of 128
+// keys with one score buffer 276; eight warps that share a tile's columns 279). One
+// warp brings K and V tiles
 // (TMA; a tile in which the keys end goes by cp.async instead, so that nothing
 // behind the lengths is read), one prepares each tile's bias.
 //
@@ -40,9 +41,10 @@
 // SM), for D = 128 the tensor cores; in front of both stands the chain of a
 // softmax warp (wait, TMEM load, maximum, exponentials, store, hand-over: ~1.9 K
 // cycles per 64 keys at D = 128). Measured: 3136 tokens of 4 clips, 12 heads of
-// 32, 170 us of 105 for the exponentials alone; 4096 causal tokens, 24 heads of
-// 64, 92 us (560 TFLOP/s); 8192 causal, 16 heads of 128, 263 us (1.05 PFLOP/s,
-// 0.62 of the measured peak). Without any exponential they take 0.82-0.87 of that.
+// 32, 171 us of 105 for the exponentials alone; 4096 causal tokens, 24 heads of
+// 64, 92 us (560 TFLOP/s); 8192 causal, 16 heads of 128, 263 us in a short run (1.05
+// PFLOP/s, 0.62 of the measured burst peak) and 301-312 us a call in a long one, under
+// the power cap. Without any exponential they take 0.82-0.87 of that.
 #include "bias_attention.cuh"
 #include "bias_attention_split.h"
 
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 2) attn_fwd_kernel(const _
 // Tiles that are split over the keys: all of them when they fill at most half of
 // the resident CTAs (two per SM); else, when all tiles cost the same, those that
 // would run as a last wave of at most half of them. As many parts as fill one
-// wave, at least 512 keys in each, or 4096 if they are two (one CTA per SM then
+// wave, at least 512 keys in each, or 4096 when two fill it (one CTA per SM then
 // runs nearly as fast as two). With and without parts: 4096 causal tokens, 2 heads
 // of 64: 23 and 42 us; 16384, 1 head: 128 and 154; the last wave of 4 x 3136, 12
 // heads of 32: 173 and 184; two parts of 4096, 4 heads: 47 and 44, hence not taken.

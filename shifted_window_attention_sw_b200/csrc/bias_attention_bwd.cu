@@ -13,9 +13,13 @@
 //
 // Measured: 4096 causal tokens, 2 x 12 heads of 64: 145 + 155 us, beside 93 of the
 // forward (the seven products that both need take 107 us at the measured peak);
-// 8 x 577 tokens, 6 heads: 29 + 25 us. Tensor cores 0.27 and 0.32 busy, special functions
-// 0.36 and 0.32, issue 0.42: bound by the chain scores - P and dS - sums of a CTA,
-// which the other CTA of the SM covers in part. Tried: one CTA per SM with two
+// 8 x 577 tokens, 6 heads: 29 + 25 us. At the first size tensor cores are 0.27 and
+// 0.32 busy, special functions 0.36 and 0.32, issue 0.42: bound by the chain scores -
+// P and dS - sums of a CTA, which the other CTA of the SM covers in part. The whole
+// call, one sequence of 4096 causal tokens: 16 heads of 128 349 us, over 4 key heads
+// 457; 32 heads of 64 393 us, over one key head 2487; 4 x 3136 tokens, 12 heads of 32:
+// 618. With few key heads the second pass has few CTAs: one per 128 keys and key head,
+// which walks all the heads that share it. Tried: one CTA per SM with two
 // groups of warps and three score buffers (163 instead of 145 us for the first
 // pass) or with three groups (slower, too: one warp issues for all), columns'
 // (lse, D) fetched a tile earlier (no change).

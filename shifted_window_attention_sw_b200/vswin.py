@@ -606,7 +606,8 @@ def bias_attention_forward(q, k, v, table, bucket_map, scale=None, causal=False,
 def bias_attention_backward(q, k, v, table, bucket_map, out, lse, dout, scale=None, causal=False, q_lens=None,
                             kv_lens=None, q_start=None, dq=None, dk=None, dv=None, stream=None):
     """Gradients (dq, dk, dv, dtable, all in the type of q) of bias_attention_forward for the output gradient
-    ``dout``, from its ``out`` and ``lse``. ``dq``, ``dk`` and ``dv`` may be given, e.g. as slices of one buffer."""
+    ``dout``, from its ``out`` and ``lse``. ``dq``, ``dk`` and ``dv`` may be given, e.g. as slices of one buffer.
+    In fp16 a small ``dout`` has to be scaled up first (see vswin_bias_attention_backward)."""
     (B, Lq, Lk, hq, hk, d, dt, dev), args = _bias_attention_args(q, k, v, table, bucket_map, scale, causal, q_lens,
                                                                  kv_lens, q_start)
     qs, ks = (B, Lq, hq, d), (B, Lk, hk, d)
@@ -718,8 +719,8 @@ class AdamW:
 
     def step(self, grads, lr=None, step=None, grad_scale=None, stream=None):
         """One step with ``grads`` (contiguous, shaped as the weights; bf16, fp16 or fp32). ``step`` counts from 1
-        (default: one more than the last) or is a one-element int32 CUDA tensor, read when the step runs, as a
-        captured step needs. grad_scale: one-element float32 CUDA tensor that multiplies every gradient."""
+        (default: one more than the last call's) or is a one-element int32 CUDA tensor, read when the step runs, as a
+        captured step needs (its lr and decays are the capture's; replays do not count in ``steps``). grad_scale: one-element float32 CUDA tensor that multiplies every gradient."""
         grads = self._list("grads", grads)
         dev = self.device
         types = [g.dtype for g in grads]
@@ -806,7 +807,8 @@ def clamp_window(T, H, W, window, shift):
 
 def poll_error(stream=None) -> int:
     """Synchronise and return the device error status (0 = OK, 4 = a kernel wait gave up,
-    6 = an index check of a VSWIN_DEBUG_BOUNDS build failed)."""
+    6 = a length, position or bucket that an operator over sequences read was out of range, or
+    an index check of a VSWIN_DEBUG_BOUNDS build failed)."""
     return int(lib().vswin_poll_error(_stream_handle(stream)))
 
 
