@@ -884,3 +884,37 @@ def test_two_layers_at_once():
                 got.append(_layer(i, kw, do, True))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("L", [1, 130, 700])
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_results_in_further_heads_of_the_inputs_buffer(d, L, heads_first):
+    # q, k, v, out, dout, dq, dk, dv and the norm's results interleave in one buffer: the same bits as apart
+    B, hq, hk = 2, 4, 2
+    ins, do = _attn_inputs(BF16, B, L, L, hq, hk, d)
+    gen = torch.Generator().manual_seed(9)
+    w = [_rand(gen, (d,), BF16) for _ in range(2)]
+    q, k, v, table = ins
+    qn, kn = vswin.qk_norm_forward(q, k, *w)
+    out, lse = vswin.bias_attention_forward(qn, kn, v, table, _map())
+    grads = vswin.bias_attention_backward(qn, kn, v, table, _map(), out, lse, do)
+    back = vswin.qk_norm_backward(q, k, *w, grads[0], grads[1])
+    sizes = dict(q=hq, qn=hq, k=hk, kn=hk, v=hk, out=hq, do=hq, dqn=hq, dkn=hk, dv=hk, dq=hq, dk=hk)
+    total = sum(sizes.values())
+    buf = torch.zeros((B, total, L, d) if heads_first else (B, L, total, d), dtype=BF16, device="cuda")
+    every, s, at = buf.transpose(1, 2) if heads_first else buf, {}, 0
+    for n, heads in sizes.items():
+        s[n] = every[:, :, at:at + heads]
+        at += heads
+    for n, x in dict(q=q, k=k, v=v, do=do).items():
+        s[n].copy_(x)
+    vswin.qk_norm_forward(s["q"], s["k"], *w, q_out=s["qn"], k_out=s["kn"])
+    o, e = vswin.bias_attention_forward(s["qn"], s["kn"], s["v"], table, _map(), out=s["out"])
+    g = vswin.bias_attention_backward(s["qn"], s["kn"], s["v"], table, _map(), o, e, s["do"], dq=s["dqn"], dk=s["dkn"],
+                                      dv=s["dv"])
+    h = vswin.qk_norm_backward(s["q"], s["k"], *w, g[0], g[1], dq=s["dq"], dk=s["dk"])
+    for n, x in dict(q=q, k=k, v=v, do=do, qn=qn, kn=kn, out=out, dqn=grads[0], dkn=grads[1], dv=grads[2], dq=back[0],
+                     dk=back[1]).items():
+        assert torch.equal(s[n], x), n
+    assert torch.equal(e, lse) and all(torch.equal(a, b) for a, b in zip((g[3], *h[2:]), (grads[3], *back[2:])))
