@@ -693,23 +693,31 @@ class AdamW:
 
     def _record(self):
         """Fills the records from the lists of weights and states as they are now."""
-        dev, states = self.device, (torch.float32, torch.float32) if self.bits == 32 else (torch.int8, torch.uint8)
-        self._recorded = None  # (until every record is right)
-        names = ("params", "m", "v", "m_scale", "v_scale", "master")
-        lists = [None if t is None else self._list(name, t) for name, t in zip(names, self._lists())]
-        for i, (r, shape) in enumerate(zip(self._records, self._shapes)):
-            at = [None if t is None else t[i] for t in lists]
-            scales = (-(-r.n // ADAMW_BLOCK),)
-            r.param = _flat(("params", i), at[0], shape, DTYPE_OF[r.param_dtype], dev)
-            r.m = _flat(("m", i), at[1], shape, states[0], dev)
-            r.v = _flat(("v", i), at[2], shape, states[1], dev)
-            r.m_scale = _flat(("m_scale", i), at[3], scales, torch.float32, dev)
-            r.v_scale = _flat(("v_scale", i), at[4], scales, torch.float32, dev)
-            r.master = _flat(("master", i), at[5], shape, torch.float32, dev)
+        self._recorded, count = None, len(self._shapes)  # (until every record is right)
+        states = (torch.float32, torch.float32) if self.bits == 32 else (torch.int8, torch.uint8)
+        scales = [(-(-r.n // ADAMW_BLOCK),) for r in self._records] if self.bits == 8 else self._shapes
+        weights = [DTYPE_OF[r.param_dtype] for r in self._records]
+        held = []
+        for name, tensors, shapes, types in zip(
+                ("params", "m", "v", "m_scale", "v_scale", "master"), self._lists(),
+                (self._shapes, self._shapes, self._shapes, scales, scales, self._shapes),
+                (weights, *([t] * count for t in (*states, torch.float32, torch.float32, torch.float32)))):
+            if tensors is None:
+                at = [0] * count
+            else:
+                tensors = self._list(name, tensors)
+                if ([t.shape for t in tensors] != shapes or [t.dtype for t in tensors] != types
+                        or list(map(_get_device, tensors)) != self._indices or not all(map(_is_contiguous, tensors))):
+                    for i, t in enumerate(tensors):
+                        _flat((name, i), t, shapes[i], types[i], self.device)
+                at = list(map(_data_ptr, tensors))
+                held.append(tensors)
+            field = _AdamwTensor.param if name == "params" else getattr(_AdamwTensor, name)
+            self._words[field.offset // 8::_RECORD_WORDS] = array.array("q", at)
         if len({r.param for r in self._records if r.n}) < sum(1 for r in self._records if r.n):
             raise ValueError("a weight stands in params twice")
         # (held, so that another tensor in a list has another address)
-        self._held, self._recorded = lists, self._addresses()
+        self._held, self._recorded = held, self._addresses()
 
     def _list(self, name, tensors):
         tensors = list(tensors)
